@@ -19,13 +19,16 @@ STATUS_NAMES = {0: "HQ_OK", 1: "HQ_ERR_INVALID_ARG", 2: "HQ_ERR_MISALIGNED", 3: 
 E4M3, E5M2 = 0, 1
 PER_TENSOR, PER_TOKEN, PER_CHANNEL = 0, 1, 2
 F32, BF16, F16 = 0, 1, 2
+ACT_NONE, ACT_RELU, ACT_GELU, ACT_GELU_TANH, ACT_SILU = 0, 1, 2, 3, 4
 
 EXPORTED = ["hq_scale_count", "hq_granularity_name", "hq_scale_pair_name", "hq_quantize_workspace_bytes",
             "hq_quantize_fp8", "hq_quantize_fp8_transpose", "hq_quantize_e5m2_stochastic",
             "hq_quantize_fp8_blockwise", "hq_dequantize_fp8_blockwise", "hq_gemm_blockscaled",
             "hq_gemm_a8w8", "hq_gemm_a8w8_ex", "hq_gemm_a8w8_blockq", "hq_grouped_gemm_a8w8", "hq_grouped_gemm_bf16",
             "hq_quantize_fp8_noalloc", "hq_quantize_fp8_delayed_batch", "hq_grad_bias",
-            "hq_grad_bias_workspace_bytes", "hq_debug_bounded_wait",
+            "hq_grad_bias_workspace_bytes", "hq_gemm_a8w8_act", "hq_act_backward_fp8",
+            "hq_act_backward_workspace_bytes", "hq_rmsnorm_fp8", "hq_rmsnorm_backward",
+            "hq_rmsnorm_backward_workspace_bytes", "hq_debug_bounded_wait",
             "hq_check_device_error", "hq_last_error", "hq_version"]
 NOALLOC_SCRATCH_BYTES = 256 * 1024
 
@@ -88,6 +91,18 @@ def _load():
     L.hq_gemm_a8w8_ex.restype = ci
     L.hq_gemm_a8w8_blockq.argtypes = [P, P, ci, P, i64, P, i64, P, i64, i64, i64, P, ci, i64, P, P]
     L.hq_gemm_a8w8_blockq.restype = ci
+    L.hq_gemm_a8w8_act.argtypes = [P, P, ci, P, i64, P, i64, P, ci, P, i64, i64, i64, P, P, ci, i64, P, P]
+    L.hq_gemm_a8w8_act.restype = ci
+    L.hq_act_backward_workspace_bytes.argtypes = [i64, i64]
+    L.hq_act_backward_workspace_bytes.restype = sz
+    L.hq_act_backward_fp8.argtypes = [P, ci, P, ci, i64, P, ci, i64, i64, P, P, P, sz, P]
+    L.hq_act_backward_fp8.restype = ci
+    L.hq_rmsnorm_fp8.argtypes = [P, ci, P, P, ci, i64, i64, ctypes.c_float, ci, i64, P, P, P, P, P, P]
+    L.hq_rmsnorm_fp8.restype = ci
+    L.hq_rmsnorm_backward_workspace_bytes.argtypes = [i64, i64]
+    L.hq_rmsnorm_backward_workspace_bytes.restype = sz
+    L.hq_rmsnorm_backward.argtypes = [P, P, ci, P, P, ci, P, i64, i64, P, P, P, sz, P]
+    L.hq_rmsnorm_backward.restype = ci
     L.hq_grouped_gemm_a8w8.argtypes = [P, P, ci, P, i64, P, i64, P, i32, i64, i64, i64, P, P]
     L.hq_grouped_gemm_a8w8.restype = ci
     L.hq_grouped_gemm_bf16.argtypes = [P, P, P, i32, i64, i64, i64, P, P]
@@ -419,6 +434,175 @@ def hq_gemm_a8w8_blockq(xq, wq, x_scale, w_scale, fmt=E4M3, bias=None, q_fmt=E4M
                                   w_scale.numel(), _ptr(bias), M, N, K, _ptr(q_out), q_fmt, block, _ptr(q_scales),
                                   _stream(stream)))
     return q_out, q_scales
+
+
+def _like(t, name, shape, dtype):
+    """A caller's buffer or operand, as the library reads it: the shape, the
+    dtype and dense rows (a strided one would be read or written wrongly)."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t
+
+
+def _out(t, name, shape, dtype, device):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    return _like(t, name, shape, dtype)
+
+
+def _matrix(t, name):
+    if t.dim() != 2:
+        raise ValueError("%s must be 2-D" % name)
+    if t.dtype not in _DT:
+        raise ValueError("%s must be float32, bfloat16 or float16" % name)
+    return t.contiguous()
+
+
+def hq_gemm_a8w8_act(xq, wq, x_scale, w_scale, fmt=E4M3, bias=None, act=ACT_NONE, residual=None, out=None,
+                     ckpt=False, z_fmt=E4M3, z_block=32, z_q=None, z_scales=None, stream=None):
+    """The a8w8 GEMM with bias, activation and residual in its epilogue:
+    out = bf16(act(z) + residual), z = x_scale w_scale (XQ . WQ^T) + bias in
+    f32.  bias bf16 [N]; residual bf16 [M, N], and out may be the residual
+    itself.  With ckpt=True (or z_q and z_scales given) z is also kept as FP8
+    codes [M, N] and dequant scales [M, N / 32], for hq_act_backward_fp8.
+    Returns out, or (out, z_q, z_scales)."""
+    if stream is not None:  # copies and buffers made here belong to that stream too
+        with torch.cuda.stream(stream):
+            return hq_gemm_a8w8_act(xq, wq, x_scale, w_scale, fmt, bias, act, residual, out, ckpt, z_fmt, z_block,
+                                    z_q, z_scales)
+    if xq.dim() != 2 or wq.dim() != 2 or wq.shape[1] != xq.shape[1]:
+        raise ValueError("xq [M, K] and wq [N, K] must be 2-D with one K")
+    xq, wq = xq.contiguous(), wq.contiguous()
+    x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
+    M, K = xq.shape
+    N = wq.shape[0]
+    _like(xq, "xq", (M, K), torch.uint8)
+    _like(wq, "wq", (N, K), torch.uint8)
+    if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
+        raise ValueError("x_scale and w_scale must be float32")
+    if bias is not None:
+        bias = _like(bias.contiguous(), "bias", (N,), torch.bfloat16)
+    if residual is not None:
+        residual = _like(residual.contiguous(), "residual", (M, N), torch.bfloat16)
+    out = _out(out, "out", (M, N), torch.bfloat16, xq.device)
+    ckpt = ckpt or z_q is not None or z_scales is not None
+    if ckpt:
+        if z_block != 32 or N % 32 != 0:
+            raise ValueError("the checkpoint takes z_block = 32 and N % 32 == 0")
+        z_q = _out(z_q, "z_q", (M, N), torch.uint8, xq.device)
+        z_scales = _out(z_scales, "z_scales", (M, N // 32), torch.float32, xq.device)
+    check(lib.hq_gemm_a8w8_act(_ptr(xq), _ptr(wq), fmt, _ptr(x_scale), x_scale.numel(), _ptr(w_scale),
+                               w_scale.numel(), _ptr(bias), act, _ptr(residual), M, N, K, _ptr(out), _ptr(z_q), z_fmt,
+                               z_block, _ptr(z_scales), _stream(None)))
+    return (out, z_q, z_scales) if ckpt else out
+
+
+def hq_act_backward_workspace_bytes(rows, cols):
+    return lib.hq_act_backward_workspace_bytes(rows, cols)
+
+
+def hq_act_backward_fp8(g, z_q, z_scales, act, fmt=E4M3, block=32, dz=None, dbias=None, need_dbias=True,
+                        workspace=None, stream=None):
+    """Backward pass of an activation from its 8-bit checkpoint: g [rows,
+    cols] the gradient of the activation's result, z_q / z_scales the
+    block-wise codes and scales of what it was applied to (hq_gemm_a8w8_act,
+    or hq_quantize_fp8_blockwise).  Returns (dz, dbias) in g's dtype, dbias
+    the column sums of dz (None with need_dbias=False).  dz may be g."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_act_backward_fp8(g, z_q, z_scales, act, fmt, block, dz, dbias, need_dbias, workspace)
+    g = _matrix(g, "g")
+    rows, cols = g.shape
+    if block <= 0:
+        raise ValueError("block must be a positive multiple of 16")
+    z_q = _like(z_q.contiguous(), "z_q", (rows, cols), torch.uint8)
+    z_scales = _like(z_scales.contiguous(), "z_scales", (rows, -(-cols // block)), torch.float32)
+    dz = _out(dz, "dz", (rows, cols), g.dtype, g.device)
+    if need_dbias:
+        dbias = _out(dbias, "dbias", (cols,), g.dtype, g.device)
+        if workspace is None:
+            workspace = torch.empty(hq_act_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=g.device)
+    elif dbias is not None:
+        raise ValueError("dbias given with need_dbias=False")
+    check(lib.hq_act_backward_fp8(_ptr(g), _DT[g.dtype], _ptr(z_q), fmt, block, _ptr(z_scales), act, rows, cols,
+                                  _ptr(dz), _ptr(dbias), _ptr(workspace), 0 if workspace is None else
+                                  workspace.numel() * workspace.element_size(), _stream(None)))
+    return dz, dbias
+
+
+def hq_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, fmt=E4M3, block=0, q=None, scales=None, residual_out=None,
+                   y_out=None, rstd_out=None, stream=None):
+    """RMS norm of h = x + residual (h = x without) with FP8 output: codes
+    and dequant scales of h * weight / rms(h), one scale per row (block=0,
+    scales [rows]) or per `block` columns (scales [rows, ceil(cols / block)]).
+    Returns (q, scales, h): h is the sum in x's dtype, in residual_out (which
+    may be x or residual itself), or x without a residual.  y_out [rows,
+    cols] and rstd_out f32 [rows], given, receive the normed values and
+    1 / rms for hq_rmsnorm_backward."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_rmsnorm_fp8(x, weight, eps, residual, fmt, block, q, scales, residual_out, y_out, rstd_out)
+    x = _matrix(x, "x")
+    rows, cols = x.shape
+    if weight.dtype not in _DT:
+        raise ValueError("weight must be float32, bfloat16 or float16")
+    weight = _like(weight.contiguous(), "weight", (cols,), weight.dtype)
+    h = x
+    if residual is not None:
+        residual = _like(residual.contiguous(), "residual", (rows, cols), x.dtype)
+        h = residual_out = _out(residual_out, "residual_out", (rows, cols), x.dtype, x.device)
+    elif residual_out is not None:
+        raise ValueError("residual_out without a residual: the sum is x itself")
+    q = _out(q, "q", (rows, cols), torch.uint8, x.device)
+    scales = _out(scales, "scales", (rows, -(-cols // block)) if block > 0 else (rows,), torch.float32, x.device)
+    if y_out is not None:
+        _like(y_out, "y_out", (rows, cols), x.dtype)
+    if rstd_out is not None:
+        _like(rstd_out, "rstd_out", (rows,), torch.float32)
+    check(lib.hq_rmsnorm_fp8(_ptr(x), _DT[x.dtype], _ptr(residual), _ptr(weight), _DT[weight.dtype], rows, cols, eps,
+                             fmt, block, _ptr(q), _ptr(scales), _ptr(residual_out), _ptr(y_out), _ptr(rstd_out),
+                             _stream(None)))
+    return q, scales, h
+
+
+def hq_rmsnorm_backward_workspace_bytes(rows, cols):
+    return lib.hq_rmsnorm_backward_workspace_bytes(rows, cols)
+
+
+def hq_rmsnorm_backward(dy, h, weight, rstd, dres=None, dx=None, dweight=None, need_dweight=True, workspace=None,
+                        stream=None):
+    """Backward pass of hq_rmsnorm_fp8's norm: dy the gradient of the normed
+    values, h and rstd as the forward call gave them, dres the gradient that
+    reaches h by other ways (or None).  Returns (dx, dweight): dx the gradient
+    of x and of residual, dweight in the weight's dtype (None with
+    need_dweight=False)."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return hq_rmsnorm_backward(dy, h, weight, rstd, dres, dx, dweight, need_dweight, workspace)
+    dy = _matrix(dy, "dy")
+    rows, cols = dy.shape
+    if weight.dtype not in _DT:
+        raise ValueError("weight must be float32, bfloat16 or float16")
+    weight = _like(weight.contiguous(), "weight", (cols,), weight.dtype)
+    h = _like(h.contiguous(), "h", (rows, cols), dy.dtype)
+    rstd = _like(rstd.contiguous(), "rstd", (rows,), torch.float32)
+    if dres is not None:
+        dres = _like(dres.contiguous(), "dres", (rows, cols), dy.dtype)
+    dx = _out(dx, "dx", (rows, cols), dy.dtype, dy.device)
+    if need_dweight:
+        dweight = _out(dweight, "dweight", (cols,), weight.dtype, dy.device)
+        if workspace is None:
+            workspace = torch.empty(hq_rmsnorm_backward_workspace_bytes(rows, cols), dtype=torch.uint8,
+                                    device=dy.device)
+    elif dweight is not None:
+        raise ValueError("dweight given with need_dweight=False")
+    check(lib.hq_rmsnorm_backward(_ptr(dy), _ptr(h), _DT[dy.dtype], _ptr(dres), _ptr(weight), _DT[weight.dtype],
+                                  _ptr(rstd), rows, cols, _ptr(dx), _ptr(dweight), _ptr(workspace),
+                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+                                  _stream(None)))
+    return dx, dweight
 
 
 def hq_grouped_gemm_a8w8(xq, wq, x_scale, w_scale, offsets, fmt=E4M3, out=None, stream=None):

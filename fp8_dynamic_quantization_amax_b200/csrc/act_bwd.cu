@@ -1,0 +1,152 @@
+// act_bwd.cu -- backward pass of an activation from its 8-bit checkpoint,
+// with the bias gradient: z = dec(z_q) * scale, dz = g * act'(z),
+// dbias = column sums of dz.  sm_100a only.
+//
+// One pass over the data.  A CTA takes a strip of 256 columns (a warp's 32
+// lanes x 8 columns) and a band of rows; warp w of the CTA takes rows w,
+// w + 8, ... of the band.  With dbias each lane adds its columns' f32 dz in
+// row order, the eight warps join in order, and the band's sums go to the
+// workspace; a second launch adds the bands in order.  The order of the sums
+// is fixed, and the workspace needs no initial state.
+#include "act.cuh"
+#include "elem.cuh"
+#include "hq_internal.cuh"
+#include "launch.cuh"
+
+#include <cuda_fp16.h>
+
+namespace hq {
+namespace {
+
+constexpr int kAbWarps = 8;
+constexpr int kAbVec = 8;                    // columns per lane
+constexpr int kAbStrip = 32 * kAbVec;        // columns per strip
+constexpr int64_t kAbMinBand = 64;           // rows per band, at least
+constexpr int64_t kAbCtas = 8 * 148;         // aim: this many CTAs
+
+__host__ __device__ inline int64_t ab_strips(int64_t cols) { return (cols + kAbStrip - 1) / kAbStrip; }
+inline int64_t ab_band_rows(int64_t rows, int64_t cols) {
+  const int64_t bands = (kAbCtas + ab_strips(cols) - 1) / ab_strips(cols);
+  const int64_t r = (rows + bands - 1) / bands;
+  return r < kAbMinBand ? kAbMinBand : r;
+}
+inline int64_t ab_bands(int64_t rows, int64_t cols) {
+  const int64_t r = ab_band_rows(rows, cols);
+  return (rows + r - 1) / r;
+}
+
+struct AbParams {
+  const void* g;
+  const uint8_t* zq;
+  const float* zs;
+  int64_t rows;
+  int cols, block, nb;
+  int64_t band_rows;
+  int strips;
+  void* dz;
+  float* part;   // [bands, cols] or null
+};
+
+// two FP8 codes (low byte first) -> two f32, exact (every code is an f16)
+template <int FMT>
+__device__ __forceinline__ float2 decode2(uint32_t c2) {
+  uint32_t h;
+  const unsigned short s = static_cast<unsigned short>(c2);
+  if (FMT == 0) asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(s));
+  else asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(h) : "h"(s));
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+
+template <int GT, int FMT, int ACT>
+__global__ void __launch_bounds__(32 * kAbWarps) k_act_bwd(const AbParams p) {
+  __shared__ float red[kAbWarps][kAbStrip];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int strip = static_cast<int>(blockIdx.x % p.strips);
+  const int64_t band = blockIdx.x / p.strips;
+  const int c0 = strip * kAbStrip + lane * kAbVec;
+  const int64_t r0 = band * p.band_rows;
+  const int64_t r1 = min(p.rows, r0 + p.band_rows);
+  float acc[kAbVec];
+#pragma unroll
+  for (int j = 0; j < kAbVec; ++j) acc[j] = 0.0f;
+  if (c0 < p.cols) {  // cols % 16 == 0: a lane's 8 columns are all inside
+    const int b = c0 / p.block;
+    for (int64_t r = r0 + warp; r < r1; r += kAbWarps) {
+      const int64_t i = r * p.cols + c0;
+      const uint2 zc = __ldg(reinterpret_cast<const uint2*>(p.zq + i));
+      const float sc = __ldg(p.zs + r * p.nb + b);
+      float g[kAbVec];
+      const char* gp = static_cast<const char*>(p.g) + i * elem_bytes<GT>();
+      vec_widen<GT>(vec_load(gp), g);
+      if (GT == 0) vec_widen<GT>(vec_load(gp + 16), g + 4);
+      float d[kAbVec];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float2 z = decode2<FMT>((j < 2 ? zc.x : zc.y) >> (16 * (j & 1)));
+        d[2 * j] = g[2 * j] * act_backward<ACT>(__fmul_rn(z.x, sc));
+        d[2 * j + 1] = g[2 * j + 1] * act_backward<ACT>(__fmul_rn(z.y, sc));
+      }
+      char* dp = static_cast<char*>(p.dz) + i * elem_bytes<GT>();
+      vec_store(dp, vec_narrow<GT>(d));
+      if (GT == 0) vec_store(dp + 16, vec_narrow<GT>(d + 4));
+#pragma unroll
+      for (int j = 0; j < kAbVec; ++j) acc[j] += d[j];
+    }
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < kAbVec; j += 4)
+    *reinterpret_cast<float4*>(&red[warp][lane * kAbVec + j]) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+  __syncthreads();
+  const int c = strip * kAbStrip + static_cast<int>(threadIdx.x);
+  if (c < p.cols) {
+    float t = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kAbWarps; ++w) t += red[w][threadIdx.x];
+    p.part[band * p.cols + c] = t;
+  }
+}
+
+template <int GT, int FMT>
+cudaError_t ab_run(const ActBwdArgs& a, const AbParams& p, unsigned grid) {
+  const dim3 b(32 * kAbWarps);
+  switch (a.act) {
+    case kActRelu: return launch_pdl(k_act_bwd<GT, FMT, kActRelu>, dim3(grid), b, 0, a.stream, false, p);
+    case kActGelu: return launch_pdl(k_act_bwd<GT, FMT, kActGelu>, dim3(grid), b, 0, a.stream, false, p);
+    case kActGeluTanh: return launch_pdl(k_act_bwd<GT, FMT, kActGeluTanh>, dim3(grid), b, 0, a.stream, false, p);
+    default: return launch_pdl(k_act_bwd<GT, FMT, kActSilu>, dim3(grid), b, 0, a.stream, false, p);
+  }
+}
+
+}  // namespace
+
+size_t act_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows == 0 || cols == 0) return 0;
+  return static_cast<size_t>(ab_bands(rows, cols)) * static_cast<size_t>(cols) * 4;
+}
+
+cudaError_t launch_act_backward(const ActBwdArgs& a) {
+  AbParams p;
+  p.g = a.g; p.zq = a.z_q; p.zs = a.z_scales; p.rows = a.rows; p.cols = static_cast<int>(a.cols);
+  p.block = static_cast<int>(a.block);
+  p.nb = static_cast<int>((a.cols + a.block - 1) / a.block);
+  p.strips = static_cast<int>(ab_strips(a.cols));
+  p.dz = a.dz;
+  p.part = a.dbias ? a.ws : nullptr;
+  int64_t bands = 0;
+  cudaError_t e = cudaSuccess;
+  if (a.rows > 0) {
+    p.band_rows = ab_band_rows(a.rows, a.cols);
+    bands = ab_bands(a.rows, a.cols);
+    const unsigned grid = static_cast<unsigned>(p.strips * bands);
+    if (a.gt == 0) e = a.fmt == 0 ? ab_run<0, 0>(a, p, grid) : ab_run<0, 1>(a, p, grid);
+    else if (a.gt == 1) e = a.fmt == 0 ? ab_run<1, 0>(a, p, grid) : ab_run<1, 1>(a, p, grid);
+    else e = a.fmt == 0 ? ab_run<2, 0>(a, p, grid) : ab_run<2, 1>(a, p, grid);
+  }
+  if (e != cudaSuccess || !a.dbias) return e;
+  return launch_column_partials(a.ws, static_cast<int>(bands), p.cols, a.dbias, a.gt, a.stream);
+}
+
+}  // namespace hq

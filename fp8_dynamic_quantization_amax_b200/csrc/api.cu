@@ -443,6 +443,163 @@ hq_status hq_grad_bias(const void* g, hq_dtype gt, int64_t rows, int64_t cols, v
                   "bias gradient launch");
 }
 
+hq_status hq_rmsnorm_fp8(const void* x, hq_dtype xt, const void* residual, const void* weight, hq_dtype wt,
+                         int64_t rows, int64_t cols, float eps, hq_fp8_format fmt, int64_t block, uint8_t* q,
+                         float* scales, void* residual_out, void* y_out, float* rstd_out, hq_stream_t stream) {
+  // ---- arguments
+  if (xt != HQ_F32 && xt != HQ_BF16 && xt != HQ_F16) return fail(HQ_ERR_INVALID_ARG, "invalid dtype %d", (int)xt);
+  if (wt != HQ_F32 && wt != HQ_BF16 && wt != HQ_F16) return fail(HQ_ERR_INVALID_ARG, "invalid weight dtype %d", (int)wt);
+  if (fmt != HQ_E4M3 && fmt != HQ_E5M2) return fail(HQ_ERR_INVALID_ARG, "invalid fp8 format %d", (int)fmt);
+  if (!(eps >= 1e-30f && eps <= 1e30f)) return fail(HQ_ERR_INVALID_ARG, "eps = %g outside [1e-30, 1e30]", (double)eps);
+  if (rows < 0 || cols < 0) return fail(HQ_ERR_INVALID_ARG, "negative shape [%lld, %lld]", (long long)rows, (long long)cols);
+  if (rows >= k2p31 || cols > hq::kNormMaxCols)
+    return fail(HQ_ERR_TOO_LARGE, "shape [%lld, %lld]: rows below 2^31, cols up to %lld", (long long)rows, (long long)cols,
+                (long long)hq::kNormMaxCols);
+  if (block < 0 || block % 16 != 0 || block >= k2p31)
+    return fail(HQ_ERR_INVALID_ARG, "block = %lld must be 0 (one scale per row) or a positive multiple of 16", (long long)block);
+  if (block > 0 && cols % 16 != 0) return fail(HQ_ERR_INVALID_ARG, "block-wise scales need cols to be a multiple of 16");
+  if (residual_out && !residual) return fail(HQ_ERR_INVALID_ARG, "residual_out without a residual: the sum is x itself");
+  if (rows == 0 || cols == 0) return ok();
+  if (!x || !weight || !q || !scales) return fail(HQ_ERR_INVALID_ARG, "x, weight, q and scales must not be null");
+  const size_t esize = (xt == HQ_F32) ? 4 : 2;
+  const size_t wsize = (wt == HQ_F32) ? 4 : 2;
+  if (!is_aligned(x, esize) || !is_aligned(residual, esize) || !is_aligned(residual_out, esize) ||
+      !is_aligned(y_out, esize) || !is_aligned(weight, wsize))
+    return fail(HQ_ERR_MISALIGNED, "x, residual, residual_out, y_out and weight must be aligned to their element size");
+  if (!is_aligned(scales, 4) || !is_aligned(rstd_out, 4))
+    return fail(HQ_ERR_MISALIGNED, "scales and rstd_out must be 4-byte aligned");
+  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(cols);
+  const size_t ns = static_cast<size_t>(rows) * static_cast<size_t>(block ? (cols + block - 1) / block : 1);
+  const Range outs[] = {{q, n, "q"}, {scales, ns * 4, "scales"}, {residual_out, n * esize, "residual_out"},
+                        {y_out, n * esize, "y_out"}, {rstd_out, static_cast<size_t>(rows) * 4, "rstd_out"}};
+  // residual_out may be x or the residual itself (each element is read before
+  // it is written, by the same thread): that pair is left out below
+  const Range ins[] = {{weight, static_cast<size_t>(cols) * wsize, "weight"},
+                       {x == residual_out ? nullptr : x, n * esize, "x"},
+                       {residual == residual_out ? nullptr : residual, n * esize, "residual"}};
+  hq_status s = check_overlaps(outs, 5, ins, 3);
+  if (s != HQ_OK) return s;
+  // ---- device
+  const Range devs[] = {{x, 0, "x"}, {residual, 0, "residual"}, {weight, 0, "weight"}, {q, 0, "q"}, {scales, 0, "scales"},
+                        {residual_out, 0, "residual_out"}, {y_out, 0, "y_out"}, {rstd_out, 0, "rstd_out"}};
+  s = check_device_ptrs(devs, 8);
+  if (s != HQ_OK) return s;
+  s = check_arch();
+  if (s != HQ_OK) return s;
+  // ---- launch
+  hq::NormArgs a;
+  a.x = x; a.xt = xt; a.residual = residual; a.weight = weight; a.wt = wt; a.rows = rows; a.cols = cols; a.eps = eps;
+  a.fmt = fmt; a.block = block; a.q = q; a.scales = scales; a.residual_out = residual_out; a.y_out = y_out;
+  a.rstd_out = rstd_out; a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return launched(hq::launch_rmsnorm(a), "RMS norm launch");
+}
+
+size_t hq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows >= k2p31 || cols > hq::kNormMaxCols) return 0;
+  return hq::rmsnorm_backward_workspace_bytes(rows, cols);
+}
+
+hq_status hq_rmsnorm_backward(const void* dy, const void* h, hq_dtype xt, const void* dres, const void* weight,
+                              hq_dtype wt, const float* rstd, int64_t rows, int64_t cols, void* dx, void* dweight,
+                              void* workspace, size_t workspace_bytes, hq_stream_t stream) {
+  // ---- arguments
+  if (xt != HQ_F32 && xt != HQ_BF16 && xt != HQ_F16) return fail(HQ_ERR_INVALID_ARG, "invalid dtype %d", (int)xt);
+  if (wt != HQ_F32 && wt != HQ_BF16 && wt != HQ_F16) return fail(HQ_ERR_INVALID_ARG, "invalid weight dtype %d", (int)wt);
+  if (rows < 0 || cols < 0) return fail(HQ_ERR_INVALID_ARG, "negative shape [%lld, %lld]", (long long)rows, (long long)cols);
+  if (rows >= k2p31 || cols > hq::kNormMaxCols)
+    return fail(HQ_ERR_TOO_LARGE, "shape [%lld, %lld]: rows below 2^31, cols up to %lld", (long long)rows, (long long)cols,
+                (long long)hq::kNormMaxCols);
+  if (cols == 0 || (rows == 0 && !dweight)) return ok();
+  if (rows > 0 && (!dy || !h || !weight || !rstd || !dx))
+    return fail(HQ_ERR_INVALID_ARG, "dy, h, weight, rstd and dx must not be null");
+  const size_t need = dweight ? hq::rmsnorm_backward_workspace_bytes(rows, cols) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(HQ_ERR_INVALID_ARG, "dweight needs a workspace of %zu bytes", need);
+  const size_t esize = (xt == HQ_F32) ? 4 : 2;
+  const size_t wsize = (wt == HQ_F32) ? 4 : 2;
+  if (!is_aligned(dy, esize) || !is_aligned(h, esize) || !is_aligned(dres, esize) || !is_aligned(dx, esize) ||
+      !is_aligned(weight, wsize) || !is_aligned(dweight, wsize))
+    return fail(HQ_ERR_MISALIGNED, "dy, h, dres, dx, weight and dweight must be aligned to their element size");
+  if (!is_aligned(rstd, 4)) return fail(HQ_ERR_MISALIGNED, "rstd must be 4-byte aligned");
+  if (need > 0 && !is_aligned(workspace, 256)) return fail(HQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(cols);
+  const Range outs[] = {{dx, n * esize, "dx"}, {dweight, static_cast<size_t>(cols) * wsize, "dweight"},
+                        {need > 0 ? workspace : nullptr, need, "workspace"}};
+  const Range ins[] = {{dy, n * esize, "dy"}, {h, n * esize, "h"}, {dres, n * esize, "dres"},
+                       {weight, static_cast<size_t>(cols) * wsize, "weight"}, {rstd, static_cast<size_t>(rows) * 4, "rstd"}};
+  hq_status s = check_overlaps(outs, 3, ins, 5);
+  if (s != HQ_OK) return s;
+  // ---- device
+  const bool any = rows > 0;
+  const Range devs[] = {{any ? dy : nullptr, 0, "dy"}, {any ? h : nullptr, 0, "h"}, {any ? dres : nullptr, 0, "dres"},
+                        {any ? weight : nullptr, 0, "weight"}, {any ? rstd : nullptr, 0, "rstd"},
+                        {any ? dx : nullptr, 0, "dx"}, {dweight, 0, "dweight"},
+                        {need > 0 ? workspace : nullptr, 0, "workspace"}};
+  s = check_device_ptrs(devs, 8);
+  if (s != HQ_OK) return s;
+  s = check_arch();
+  if (s != HQ_OK) return s;
+  // ---- launch
+  hq::NormBwdArgs a;
+  a.dy = dy; a.h = h; a.xt = xt; a.dres = dres; a.weight = weight; a.wt = wt; a.rstd = rstd; a.rows = rows; a.cols = cols;
+  a.dx = dx; a.dweight = dweight; a.ws = static_cast<float*>(workspace); a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return launched(hq::launch_rmsnorm_backward(a), "RMS norm backward launch");
+}
+
+size_t hq_act_backward_workspace_bytes(int64_t rows, int64_t cols) {
+  if (rows < 0 || cols < 0 || rows >= k2p31 || cols >= k2p31) return 0;
+  return hq::act_backward_workspace_bytes(rows, cols);
+}
+
+hq_status hq_act_backward_fp8(const void* g, hq_dtype gt, const uint8_t* z_q, hq_fp8_format z_fmt, int64_t z_block,
+                              const float* z_scales, hq_activation act, int64_t rows, int64_t cols, void* dz, void* dbias,
+                              void* workspace, size_t workspace_bytes, hq_stream_t stream) {
+  // ---- arguments
+  if (gt != HQ_F32 && gt != HQ_BF16 && gt != HQ_F16) return fail(HQ_ERR_INVALID_ARG, "invalid dtype %d", (int)gt);
+  if (z_fmt != HQ_E4M3 && z_fmt != HQ_E5M2) return fail(HQ_ERR_INVALID_ARG, "invalid fp8 format %d", (int)z_fmt);
+  if (act <= HQ_ACT_NONE || act > HQ_ACT_SILU)
+    return fail(HQ_ERR_INVALID_ARG, "activation %d has no backward pass here", (int)act);
+  if (rows < 0 || cols < 0) return fail(HQ_ERR_INVALID_ARG, "negative shape [%lld, %lld]", (long long)rows, (long long)cols);
+  if (rows >= k2p31 || cols >= k2p31 || (cols > 0 && rows > (k2p40 - 1) / cols))
+    return fail(HQ_ERR_TOO_LARGE, "shape [%lld, %lld] is beyond the supported range", (long long)rows, (long long)cols);
+  if (z_block < 16 || z_block % 16 != 0 || z_block >= k2p31)
+    return fail(HQ_ERR_INVALID_ARG, "block = %lld must be a positive multiple of 16", (long long)z_block);
+  if (cols % 16 != 0) return fail(HQ_ERR_INVALID_ARG, "cols must be a multiple of 16");
+  if (cols == 0 || (rows == 0 && !dbias)) return ok();
+  if (rows > 0 && (!g || !z_q || !z_scales || !dz)) return fail(HQ_ERR_INVALID_ARG, "g, z_q, z_scales and dz must not be null");
+  const size_t need = dbias ? hq::act_backward_workspace_bytes(rows, cols) : 0;
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(HQ_ERR_INVALID_ARG, "dbias needs a workspace of %zu bytes", need);
+  const size_t esize = (gt == HQ_F32) ? 4 : 2;
+  if (!is_aligned(g, 16) || !is_aligned(z_q, 16) || !is_aligned(dz, 16))
+    return fail(HQ_ERR_MISALIGNED, "g, z_q and dz must be 16-byte aligned");
+  if (!is_aligned(dbias, esize)) return fail(HQ_ERR_MISALIGNED, "dbias must be aligned to its element size");
+  if (!is_aligned(z_scales, 4)) return fail(HQ_ERR_MISALIGNED, "z_scales must be 4-byte aligned");
+  if (need > 0 && !is_aligned(workspace, 256)) return fail(HQ_ERR_MISALIGNED, "workspace must be 256-byte aligned");
+  const size_t n = static_cast<size_t>(rows) * static_cast<size_t>(cols);
+  const size_t ns = static_cast<size_t>(rows) * static_cast<size_t>((cols + z_block - 1) / z_block);
+  const Range outs[] = {{dz, n * esize, "dz"}, {dbias, static_cast<size_t>(cols) * esize, "dbias"},
+                        {need > 0 ? workspace : nullptr, need, "workspace"}};
+  // dz may be g itself (each element is read before it is written, by the same thread)
+  const Range ins[] = {{z_q, n, "z_q"}, {z_scales, ns * 4, "z_scales"}, {g == dz ? nullptr : g, n * esize, "g"}};
+  hq_status s = check_overlaps(outs, 3, ins, 3);
+  if (s != HQ_OK) return s;
+  // ---- device
+  const bool any = rows > 0;
+  const Range devs[] = {{any ? g : nullptr, 0, "g"}, {any ? z_q : nullptr, 0, "z_q"}, {any ? z_scales : nullptr, 0, "z_scales"},
+                        {any ? dz : nullptr, 0, "dz"}, {dbias, 0, "dbias"}, {need > 0 ? workspace : nullptr, 0, "workspace"}};
+  s = check_device_ptrs(devs, 6);
+  if (s != HQ_OK) return s;
+  s = check_arch();
+  if (s != HQ_OK) return s;
+  // ---- launch
+  hq::ActBwdArgs a;
+  a.g = g; a.gt = gt; a.z_q = z_q; a.fmt = z_fmt; a.block = z_block; a.z_scales = z_scales; a.act = act;
+  a.rows = rows; a.cols = cols; a.dz = dz; a.dbias = dbias; a.ws = static_cast<float*>(workspace);
+  a.stream = reinterpret_cast<cudaStream_t>(stream);
+  return launched(hq::launch_act_backward(a), "activation backward launch");
+}
+
 hq_status hq_quantize_e5m2_stochastic(const void* x, hq_dtype xt, int64_t rows, int64_t cols, hq_granularity g,
                                       uint64_t seed, uint8_t* q, float* scales, float* amax_out, void* workspace,
                                       size_t workspace_bytes, hq_stream_t stream) {
@@ -566,6 +723,14 @@ struct GemmEx {
   bool blockq = false;         // block-wise FP8 output (no ring) into q_out and q_bscales
   float* q_bscales = nullptr;  // dequant scales [M, N / q_block]
   int64_t q_block = 0;
+  // activation epilogue (bf16 out; no ring, no FP8 output)
+  bool act_epilogue = false;
+  int act = 0;
+  const void* residual = nullptr;
+  uint8_t* z_q = nullptr;
+  int z_fmt = 0;
+  int64_t z_block = 0;
+  float* z_scales = nullptr;
 };
 
 hq_status gemm_common(int kind, const void* a, const void* b, int fmt, const float* xs, int64_t xs_len,
@@ -601,8 +766,22 @@ hq_status gemm_common(int kind, const void* a, const void* b, int fmt, const flo
   size_t need = 0;
   if (ex) {
     if (grouped) return fail(HQ_ERR_INVALID_ARG, "fused epilogues are for the dense GEMM");
-    if (fp8o == (out != nullptr)) return fail(HQ_ERR_INVALID_ARG, "exactly one of out and q_out must be given");
+    if (fp8o == (out != nullptr) && !(ex->act_epilogue && empty))
+      return fail(HQ_ERR_INVALID_ARG, "exactly one of out and q_out must be given");
     if (ex->bias && !is_aligned(ex->bias, 4)) return fail(HQ_ERR_MISALIGNED, "bias must be 4-byte aligned");
+    if (ex->act_epilogue) {
+      if (ex->act < HQ_ACT_NONE || ex->act > HQ_ACT_SILU) return fail(HQ_ERR_INVALID_ARG, "invalid activation %d", ex->act);
+      if (!is_aligned(ex->residual, 16)) return fail(HQ_ERR_MISALIGNED, "residual must start on a 16-byte boundary");
+      if ((ex->z_q != nullptr) != (ex->z_scales != nullptr))
+        return fail(HQ_ERR_INVALID_ARG, "z_q and z_scales must be given together");
+      if (ex->z_q) {
+        if (ex->z_fmt != HQ_E4M3 && ex->z_fmt != HQ_E5M2) return fail(HQ_ERR_INVALID_ARG, "invalid z_fmt %d", ex->z_fmt);
+        if (ex->z_block != 32) return fail(HQ_ERR_INVALID_ARG, "z_block = %lld: only 32 is supported", (long long)ex->z_block);
+        if (N % 32 != 0) return fail(HQ_ERR_INVALID_ARG, "N = %lld must be a multiple of the block (32)", (long long)N);
+        if (!is_aligned(ex->z_q, 16)) return fail(HQ_ERR_MISALIGNED, "z_q must start on a 16-byte boundary");
+        if (!is_aligned(ex->z_scales, 4)) return fail(HQ_ERR_MISALIGNED, "z_scales must be 4-byte aligned");
+      }
+    }
     if (fp8o && bq) {
       if (ex->q_fmt != HQ_E4M3 && ex->q_fmt != HQ_E5M2)
         return fail(HQ_ERR_INVALID_ARG, "invalid q_fmt %d", ex->q_fmt);
@@ -633,34 +812,46 @@ hq_status gemm_common(int kind, const void* a, const void* b, int fmt, const flo
     }
   }
   void* dst = fp8o ? static_cast<void*>(ex->q_out) : out;
-  if ((!dst && !(fp8o && empty)) || (K > 0 && ((!a && M > 0) || (!b && N > 0))))
+  if ((!dst && !((fp8o || (ex != nullptr && ex->act_epilogue)) && empty)) || (K > 0 && ((!a && M > 0) || (!b && N > 0))))
     return fail(HQ_ERR_INVALID_ARG, "operand and output pointers must not be null");
   if (!is_aligned(dst, 16)) return fail(HQ_ERR_MISALIGNED, "out must start on a 16-byte boundary");
   if (!is_aligned(a, 16) || !is_aligned(b, 16)) return fail(HQ_ERR_MISALIGNED, "A and B must be 16-byte aligned");
   if (offsets && !is_aligned(offsets, 4)) return fail(HQ_ERR_MISALIGNED, "offsets must be 4-byte aligned");
   const int64_t ebatch = grouped ? E : 1;
   const bool dq = fp8o && !bq;  // delayed per-tensor FP8 output
+  const bool zck = ex != nullptr && ex->z_q != nullptr;  // 8-bit checkpoint beside the output
   const Range outs[] = {{dst, static_cast<size_t>(M) * static_cast<size_t>(N) * (fp8o ? 1 : 2), fp8o ? "q_out" : "out"},
                         {dq ? ex->q_scale : nullptr, 4, "q_scale"},
                         {dq ? ex->q_amax : nullptr, 4, "q_amax"},
                         {dq ? ex->ring : nullptr, dq ? static_cast<size_t>(ex->ring_len + 2) * 4 : 0, "ring"},
                         {dq ? ex->workspace : nullptr, need, "workspace"},
                         {bq ? ex->q_bscales : nullptr, bq ? static_cast<size_t>(M) * static_cast<size_t>(N / 32) * 4 : 0,
-                         "q_scales"}};
+                         "q_scales"},
+                        {zck ? ex->z_q : nullptr, zck ? static_cast<size_t>(M) * static_cast<size_t>(N) : 0, "z_q"},
+                        {zck ? ex->z_scales : nullptr,
+                         zck ? static_cast<size_t>(M) * static_cast<size_t>(N / 32) * 4 : 0, "z_scales"}};
   const Range ins[] = {{a, static_cast<size_t>(M * K * esize), "A"},
                        {b, static_cast<size_t>(ebatch * N * K * esize), "B"},
                        {xs, kind == 0 ? static_cast<size_t>(xs_len) * 4 : 0, "x_scale"},
                        {ws, kind == 0 ? static_cast<size_t>(ws_len) * 4 : 0, "w_scale"},
                        {offsets, offsets ? static_cast<size_t>(E + 1) * 4 : 0, "offsets"},
                        {ex ? ex->bias : nullptr, static_cast<size_t>(N) * 2, "bias"}};
-  hq_status s = check_overlaps(outs, 6, ins, 6);
+  hq_status s = check_overlaps(outs, 8, ins, 6);
   if (s != HQ_OK) return s;
+  if (ex && ex->residual) {  // out may be the residual itself; no other overlap
+    const Range res = {ex->residual, static_cast<size_t>(M) * static_cast<size_t>(N) * 2, "residual"};
+    for (const Range& o : outs)
+      if (!(o.p == out && o.p == res.p) && overlaps(o, res))
+        return fail(HQ_ERR_OVERLAP, "%s overlaps residual", o.name);
+  }
   const Range devs[] = {{a, 0, "A"}, {b, 0, "B"}, {xs, 0, "x_scale"}, {ws, 0, "w_scale"},
                         {offsets, 0, "offsets"}, {dst, 0, "out"}, {ex ? ex->bias : nullptr, 0, "bias"},
                         {dq ? ex->q_scale : nullptr, 0, "q_scale"}, {dq ? ex->q_amax : nullptr, 0, "q_amax"},
                         {dq ? ex->ring : nullptr, 0, "ring"}, {dq ? ex->workspace : nullptr, 0, "workspace"},
-                        {bq ? ex->q_bscales : nullptr, 0, "q_scales"}};
-  s = check_device_ptrs(devs, 12);
+                        {bq ? ex->q_bscales : nullptr, 0, "q_scales"},
+                        {ex ? ex->residual : nullptr, 0, "residual"},
+                        {zck ? ex->z_q : nullptr, 0, "z_q"}, {zck ? ex->z_scales : nullptr, 0, "z_scales"}};
+  s = check_device_ptrs(devs, 15);
   if (s != HQ_OK) return s;
   s = check_arch();
   if (s != HQ_OK) return s;
@@ -683,6 +874,10 @@ hq_status gemm_common(int kind, const void* a, const void* b, int fmt, const flo
   g.stream = reinterpret_cast<cudaStream_t>(stream);
   if (ex) {
     g.bias = ex->bias;
+    g.act_epilogue = ex->act_epilogue;
+    g.act = ex->act;
+    g.residual = ex->residual;
+    g.z_q = ex->z_q; g.z_fmt = ex->z_fmt; g.z_scales = ex->z_scales;
     if (bq) {
       g.out = nullptr;
       g.q_out = ex->q_out; g.q_fmt = ex->q_fmt; g.q_bscales = ex->q_bscales;
@@ -725,6 +920,22 @@ hq_status hq_gemm_a8w8_blockq(const uint8_t* xq, const uint8_t* wq, hq_fp8_forma
   ex.q_bscales = q_scales;
   ex.q_block = block;
   return gemm_common(0, xq, wq, fmt, x_scale, x_scale_len, w_scale, w_scale_len, nullptr, 1, M, N, K, nullptr, stream,
+                     &ex);
+}
+
+hq_status hq_gemm_a8w8_act(const uint8_t* xq, const uint8_t* wq, hq_fp8_format fmt, const float* x_scale,
+                           int64_t x_scale_len, const float* w_scale, int64_t w_scale_len, const void* bias,
+                           hq_activation act, const void* residual, int64_t M, int64_t N, int64_t K, void* out,
+                           uint8_t* z_q, hq_fp8_format z_fmt, int64_t z_block, float* z_scales, hq_stream_t stream) {
+  GemmEx ex{bias, nullptr, 0, nullptr, nullptr, nullptr, 0, 0, 0, nullptr, 0};
+  ex.act_epilogue = true;
+  ex.act = static_cast<int>(act);
+  ex.residual = residual;
+  ex.z_q = z_q;
+  ex.z_fmt = static_cast<int>(z_fmt);
+  ex.z_block = z_block;
+  ex.z_scales = z_scales;
+  return gemm_common(0, xq, wq, fmt, x_scale, x_scale_len, w_scale, w_scale_len, nullptr, 1, M, N, K, out, stream,
                      &ex);
 }
 

@@ -21,6 +21,7 @@
 //               tile i overlap the main loop of tile i+1.
 // Every wait is bounded: on a stalled barrier the CTA records an error in a
 // device word, drains what it has in flight and exits instead of hanging.
+#include "act.cuh"
 #include "fp8_cvt.cuh"
 #include "hq_internal.cuh"
 #include "launch.cuh"
@@ -75,6 +76,13 @@ struct Params {
   // block-wise FP8 output instead of the ring: each row's 32-column blocks
   // quantized on their own, dequant scales [M, N / 32]
   float* qbs;
+  // activation epilogue: out = bf16(act(z) + res), z = acc * scales + bias,
+  // and z as block-wise FP8 (32-column blocks of a row) when zq is set
+  int act;
+  const uint16_t* res;   // bf16 [M, N] or null; may be out itself
+  uint8_t* zq;           // codes [M, N] or null
+  float* zs;             // dequant scales [M, N / 32]
+  int zfmt;
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -356,6 +364,138 @@ __device__ __forceinline__ void epilogue_chunks(uint32_t tacc, int half, int lan
   }
 }
 
+// 16 bytes that this kernel may also write (the residual may be out itself):
+// a plain load, in program order with the stores.
+__device__ __forceinline__ uint4 ld_global_v4(const void* p) {
+  uint4 u;
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p) : "memory");
+  return u;
+}
+
+// The 32 columns of a lane's row as FP8 codes with one scale: amax over the
+// finite |z|, m = fmax / amax (1 when amax is 0 or the quotient is not
+// finite), saturating RNE, NaN -> 0x7F.  z is quantized in f32, without the
+// bf16 rounding that a stored result takes: the codes are rounded once.
+__device__ __forceinline__ float chunk_f32_to_fp8(const float (&z)[32], int fmt, uint32_t (&c4)[8]) {
+  uint32_t mx = 0;
+#pragma unroll
+  for (int j = 0; j < 32; ++j) mx = max(mx, __float_as_uint(z[j]) & 0x7FFFFFFFu);
+  const bool special = mx >= 0x7F800000u;
+  if (special) {
+    mx = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) mx = max(mx, __float_as_uint(finite_abs(z[j])));
+  }
+  const float a = __uint_as_float(mx);
+  float m = 1.0f;
+  if (a > 0.0f) {
+    m = __fdiv_rn(fmt == 0 ? kFmaxE4M3 : kFmaxE5M2, a);
+    if (!(m <= FLT_MAX)) m = 1.0f;
+  }
+#pragma unroll
+  for (int j = 0; j < 16; ++j) {
+    const float lo = __fmul_rn(z[2 * j], m), hi = __fmul_rn(z[2 * j + 1], m);
+    uint32_t c2;
+    if (special) c2 = (fmt == 0) ? cvt2_exact<0>(lo, hi) : cvt2_exact<1>(lo, hi);
+    else c2 = (fmt == 0) ? cvt2_fast<0>(lo, hi) : cvt2_fast<1>(lo, hi);
+    c4[j >> 1] = (j & 1) ? (c4[j >> 1] | (c2 << 16)) : c2;
+  }
+  return m;
+}
+
+template <int ACT>
+__device__ __forceinline__ void chunk_act(float (&z)[32]) {
+#pragma unroll
+  for (int j = 0; j < 32; ++j) z[j] = act_forward<ACT>(z[j]);
+}
+
+// One epilogue warp's share of a tile with the activation epilogue: as
+// epilogue_chunks, but z = acc * scales (+ bias) stays in f32 through the
+// checkpoint's quantize, the activation and the residual addition, and is
+// rounded to bf16 once.
+template <int kChunks>
+__device__ __forceinline__ void epilogue_chunks_act(uint32_t tacc, int half, int lane, int col0, int col_end,
+                                                    int tile_end, int row0, int row, bool vrow, bool tma_ok,
+                                                    bool has_acc, float xsv, const float* wsh, const Params& p,
+                                                    uint8_t* sb, const CUtensorMap* tm_out, uint64_t out_pol) {
+  const int64_t rbase = static_cast<int64_t>(vrow ? row : 0) * p.N;
+  uint16_t* orow = p.out + rbase;
+#pragma unroll 1
+  for (int j = 0; half + 2 * j < kChunks; ++j) {
+    const int n0 = col0 + (half + 2 * j) * 32;
+    uint32_t v[32];
+    tmem_ld32(tacc + static_cast<uint32_t>((half + 2 * j) * 32), v);
+    if (n0 >= col_end) continue;
+    const float* sc = wsh + j * 32;
+    float z[32];
+    if (p.bias == nullptr) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        scale2(has_acc ? __uint_as_float(v[2 * k]) : 0.0f, has_acc ? __uint_as_float(v[2 * k + 1]) : 0.0f, sc[2 * k],
+               sc[2 * k + 1], xsv, z[2 * k], z[2 * k + 1]);
+    } else {
+      const uint32_t* bp = reinterpret_cast<const uint32_t*>(p.bias) + (n0 >> 1);
+#pragma unroll
+      for (int k = 0; k < 16; ++k) {
+        const uint32_t bb = (n0 + 2 * k < p.N) ? __ldg(bp + k) : 0u;
+        scale2_bias(has_acc ? __uint_as_float(v[2 * k]) : 0.0f, has_acc ? __uint_as_float(v[2 * k + 1]) : 0.0f,
+                    sc[2 * k], sc[2 * k + 1], xsv, __uint_as_float(bb << 16), __uint_as_float(bb & 0xFFFF0000u),
+                    z[2 * k], z[2 * k + 1]);
+      }
+    }
+    if (p.zq != nullptr) {  // N % 32 == 0: the chunk is one whole block of the row
+      uint32_t c4[8];
+      const float m = chunk_f32_to_fp8(z, p.zfmt, c4);
+      if (vrow) {
+        st_global_v4(p.zq + rbase + n0, c4[0], c4[1], c4[2], c4[3]);
+        st_global_v4(p.zq + rbase + n0 + 16, c4[4], c4[5], c4[6], c4[7]);
+        p.zs[static_cast<int64_t>(row) * (p.N >> 5) + (n0 >> 5)] = __fdiv_rn(1.0f, m);
+      }
+    }
+    switch (p.act) {
+      case kActRelu: chunk_act<kActRelu>(z); break;
+      case kActGelu: chunk_act<kActGelu>(z); break;
+      case kActGeluTanh: chunk_act<kActGeluTanh>(z); break;
+      case kActSilu: chunk_act<kActSilu>(z); break;
+      default: break;
+    }
+    if (p.res != nullptr && vrow) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (n0 + 8 * k >= col_end) break;
+        const uint4 u = ld_global_v4(p.res + rbase + n0 + 8 * k);
+        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          z[8 * k + 2 * i] += __uint_as_float(w4[i] << 16);
+          z[8 * k + 2 * i + 1] += __uint_as_float(w4[i] & 0xFFFF0000u);
+        }
+      }
+    }
+    uint32_t w[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
+    if (tma_ok && n0 + 32 <= tile_end) {  // staging tile and TMA store, as epilogue_chunks
+      if (lane == 0) bulk_wait_read_le0();
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        st_shared_v4(sb + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2],
+                     w[4 * k + 3]);
+      ptx::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        tma_store_2d(tm_out, sb, n0, row0, out_pol);
+        bulk_commit_group();
+      }
+    } else if (vrow) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (n0 + 8 * k < col_end) st_global_v4(orow + n0 + 8 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+    }
+  }
+}
+
 // ------------------------------------------------------------ tile schedule
 struct Tile {
   int a_row;   // first A row loaded (global)
@@ -439,7 +579,8 @@ __device__ void build_tile_prefix(const Params& p, int* prefix, int* starts) {
 // KPS: consecutive K blocks per pipeline stage.  With KPS > 1 each stage asks
 // DRAM for KPS * 128 contiguous bytes of every weight row at once instead of
 // one 128-byte piece per row, so more of each opened DRAM page is used.
-template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1>
+// ACT: the activation epilogue (dense a8w8 only) instead of the plain one.
+template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1, bool ACT = false>
 __global__ void __launch_bounds__(kGemm1Threads, 1)
     k_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
            const __grid_constant__ CUtensorMap tm_out, const Params p) {
@@ -652,10 +793,14 @@ __global__ void __launch_bounds__(kGemm1Threads, 1)
       uint16_t* orow = p.out + static_cast<int64_t>(vrow ? row : 0) * p.N;
       uint8_t* qrow = (KIND == 0 && p.qout != nullptr) ? p.qout + static_cast<int64_t>(vrow ? row : 0) * p.N : nullptr;
       float* qsrow = (KIND == 0 && p.qbs != nullptr) ? p.qbs + static_cast<int64_t>(vrow ? row : 0) * (p.N >> 5) : nullptr;
-      epilogue_chunks<KIND, kChunks>(
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride, half, lane,
-          T.col0, ncap, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv, wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out,
-          out_pol);
+      const uint32_t tacc =
+          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride;
+      if constexpr (ACT)
+        epilogue_chunks_act<kChunks>(tacc, half, lane, T.col0, ncap, T.col0 + BN, row0, row, vrow, tma_ok, has_acc, xsv,
+                                     wsh, p, sb, &tm_out, out_pol);
+      else
+        epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, ncap, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
+                                       wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty_bar[acc]);
@@ -744,9 +889,14 @@ void set_fused_epilogue(const GemmArgs& a, Params& p) {
   p.ring_margin = a.ring_margin;
   p.qws = a.q_ws;
   p.qbs = a.q_bscales;
+  p.act = a.act;
+  p.res = static_cast<const uint16_t*>(a.residual);
+  p.zq = a.z_q;
+  p.zs = a.z_scales;
+  p.zfmt = a.z_fmt;
 }
 
-template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1>
+template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1, bool ACT = false>
 cudaError_t run(const GemmArgs& a, std::string* msg) {
   constexpr int kElem = (KIND == 0) ? 1 : 2;
   constexpr int kSmem = STAGES * KPS * (AROWS + BN) * kBKBytes + 8 * 2048 + 8 * (((BN + 31) / 32 + 1) / 2) * 32 * 4 + 1024;
@@ -755,7 +905,7 @@ cudaError_t run(const GemmArgs& a, std::string* msg) {
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
     attr_err =
-        cudaFuncSetAttribute(k_gemm<KIND, BN, STAGES, AROWS, KPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncSetAttribute(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   });
   if (attr_err != cudaSuccess) {
     *msg = "cudaFuncSetAttribute failed";
@@ -808,7 +958,7 @@ cudaError_t run(const GemmArgs& a, std::string* msg) {
     tiles_bound = (static_cast<int64_t>(p.m_tiles) + a.E) * p.n_tiles;
   int grid = static_cast<int>(tiles_bound < sms ? tiles_bound : sms);
   if (grid < 1) grid = 1;
-  return launch_pdl(k_gemm<KIND, BN, STAGES, AROWS, KPS>, dim3(grid), dim3(kGemm1Threads), kSmem, a.stream, false,
+  return launch_pdl(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, dim3(grid), dim3(kGemm1Threads), kSmem, a.stream, false,
                     ta, tb, to, p);
 }
 
@@ -876,7 +1026,7 @@ __device__ __forceinline__ void mma_issue_pair(uint32_t d_tmem, uint64_t adesc, 
 // tile i's epilogue overlaps tile i+1's main loop.  NSUB = 2: each K step issues two
 // MMAs against the same A stage (fewer operand bytes per flop) into one
 // accumulator of up to 512 columns; the epilogue then does not overlap.
-template <int KIND, int SUBN, int NSUB, int STAGES>
+template <int KIND, int SUBN, int NSUB, int STAGES, bool ACT = false>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     k_gemm2(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const Params p) {
@@ -1103,10 +1253,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       uint16_t* orow = p.out + static_cast<int64_t>(vrow ? row : 0) * p.N;
       uint8_t* qrow = (KIND == 0 && p.qout != nullptr) ? p.qout + static_cast<int64_t>(vrow ? row : 0) * p.N : nullptr;
       float* qsrow = (KIND == 0 && p.qbs != nullptr) ? p.qbs + static_cast<int64_t>(vrow ? row : 0) * (p.N >> 5) : nullptr;
-      epilogue_chunks<KIND, kChunks>(
-          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride, half, lane,
-          T.col0, p.N, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv, wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out,
-          out_pol);
+      const uint32_t tacc =
+          tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride;
+      if constexpr (ACT)
+        epilogue_chunks_act<kChunks>(tacc, half, lane, T.col0, p.N, T.col0 + BN, row0, row, vrow, tma_ok, has_acc, xsv,
+                                     wsh, p, sb, &tm_out, out_pol);
+      else
+        epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, p.N, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
+                                       wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
@@ -1127,7 +1281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-template <int KIND, int SUBN, int NSUB, int STAGES>
+template <int KIND, int SUBN, int NSUB, int STAGES, bool ACT = false>
 cudaError_t run2(const GemmArgs& a, std::string* msg) {
   constexpr int BN = SUBN * NSUB;
   constexpr int kElem = (KIND == 0) ? 1 : 2;
@@ -1139,7 +1293,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   static int max_clusters = 0;
   std::call_once(once, [] {
     attr_err =
-        cudaFuncSetAttribute(k_gemm2<KIND, SUBN, NSUB, STAGES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaFuncSetAttribute(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(148, 1, 1);
@@ -1152,7 +1306,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&max_clusters, k_gemm2<KIND, SUBN, NSUB, STAGES>, &cfg) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveClusters(&max_clusters, k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
       max_clusters = 0;
     }
@@ -1205,13 +1359,13 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   const int64_t tiles = static_cast<int64_t>(p.m_tiles + (a.offsets != nullptr ? a.E : 0)) * p.n_tiles;
   if (tiles < clusters) clusters = static_cast<int>(tiles);
   if (clusters < 1) clusters = 1;
-  return launch_pdl(k_gemm2<KIND, SUBN, NSUB, STAGES>, dim3(2 * clusters), dim3(kGemmThreads), kSmem, a.stream,
+  return launch_pdl(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, dim3(2 * clusters), dim3(kGemmThreads), kSmem, a.stream,
                     false, ta, tb, to, p);
 }
 
-}  // namespace
-
-cudaError_t launch_gemm(const GemmArgs& a, std::string* msg) {
+// ACT: the kernels with the activation epilogue (dense a8w8; the same tiles).
+template <bool ACT>
+cudaError_t dispatch_gemm(const GemmArgs& a, std::string* msg) {
   // Wide tiles when there is enough work to fill the machine with them.
   // 256-wide tiles halve the A bytes per MMA cycle; worth a ragged last N
   // tile once N is large enough
@@ -1225,8 +1379,8 @@ cudaError_t launch_gemm(const GemmArgs& a, std::string* msg) {
                     (a.M >= 4096 || (a.M >= 512 && static_cast<double>(a.M) * a.N * a.K >= 137438953472.0));  // 2^37
   // 256 x 512 pair tiles read a quarter fewer operand bytes per flop; with
   // enough M their coarser last round costs little
-  if (pair && a.N % 512 == 0 && a.M >= 8192) return run2<0, 256, 2, 4>(a, msg);
-  if (pair) return run2<0, 256, 1, 6>(a, msg);
+  if (pair && a.N % 512 == 0 && a.M >= 8192) return run2<0, 256, 2, 4, ACT>(a, msg);
+  if (pair) return run2<0, 256, 1, 6, ACT>(a, msg);
   // Grouped GEMMs with wide experts run on CTA pairs too: 256-row tiles per
   // expert, one third fewer operand bytes per flop than 128 x 256 tiles.
   if (a.offsets != nullptr && a.N >= 1024 && a.M >= 512) {
@@ -1243,35 +1397,42 @@ cudaError_t launch_gemm(const GemmArgs& a, std::string* msg) {
     int dev = 0;
     cudaGetDevice(&dev);
     const int64_t sms = device_sm_count(dev);
-    // (a block-wise FP8 output needs tiles that start on its 32-column
-    // blocks: 256 instead of 208)
+    // (block-wise FP8 codes, of the result or of the checkpoint, need tiles
+    // that start on their 32-column blocks: 256 instead of 208)
     const int bn = ((a.N + 63) / 64 <= sms)                              ? 64
                    : ((a.N + 127) / 128 <= sms)                          ? 128
-                   : ((a.N + 207) / 208 <= sms && a.q_bscales == nullptr) ? 208
-                                                                          : 256;
+                   : ((a.N + 207) / 208 <= sms && a.q_bscales == nullptr && a.z_q == nullptr)
+                       ? 208
+                       : 256;
     if (a.M <= 16) {
-      if (bn == 64) return run<0, 64, 2, 16, 8>(a, msg);
-      if (bn == 128) return run<0, 128, 3, 16, 3>(a, msg);
-      if (bn == 208) return run<0, 208, 3, 16, 2>(a, msg);
-      return run<0, 256, 2, 16, 2>(a, msg);
+      if (bn == 64) return run<0, 64, 2, 16, 8, ACT>(a, msg);
+      if (bn == 128) return run<0, 128, 3, 16, 3, ACT>(a, msg);
+      if (bn == 208) return run<0, 208, 3, 16, 2, ACT>(a, msg);
+      return run<0, 256, 2, 16, 2, ACT>(a, msg);
     }
     if (a.M <= 64) {
-      if (bn == 64) return run<0, 64, 3, 64, 4>(a, msg);
-      if (bn == 128) return run<0, 128, 2, 64, 4>(a, msg);
-      if (bn == 208) return run<0, 208, 2, 64, 2>(a, msg);
-      return run<0, 256, 2, 64, 2>(a, msg);
+      if (bn == 64) return run<0, 64, 3, 64, 4, ACT>(a, msg);
+      if (bn == 128) return run<0, 128, 2, 64, 4, ACT>(a, msg);
+      if (bn == 208) return run<0, 208, 2, 64, 2, ACT>(a, msg);
+      return run<0, 256, 2, 64, 2, ACT>(a, msg);
     }
-    if (bn == 64) return run<0, 64, 2, 128, 4>(a, msg);
-    if (bn == 128) return run<0, 128, 3, 128, 2>(a, msg);
-    if (bn == 208) return run<0, 208, 4, 128, 1>(a, msg);
-    return run<0, 256, 4>(a, msg);
+    if (bn == 64) return run<0, 64, 2, 128, 4, ACT>(a, msg);
+    if (bn == 128) return run<0, 128, 3, 128, 2, ACT>(a, msg);
+    if (bn == 208) return run<0, 208, 4, 128, 1, ACT>(a, msg);
+    return run<0, 256, 4, kBM, 1, ACT>(a, msg);
   }
   if (a.kind == 0) {
-    if (wide) return run<0, 256, 4>(a, msg);
-    return run<0, 128, 6>(a, msg);
+    if (wide) return run<0, 256, 4, kBM, 1, ACT>(a, msg);
+    return run<0, 128, 6, kBM, 1, ACT>(a, msg);
   }
   if (wide) return run<1, 256, 4>(a, msg);
   return run<1, 128, 6>(a, msg);
+}
+
+}  // namespace
+
+cudaError_t launch_gemm(const GemmArgs& a, std::string* msg) {
+  return a.act_epilogue ? dispatch_gemm<true>(a, msg) : dispatch_gemm<false>(a, msg);
 }
 
 unsigned* device_error_word() {

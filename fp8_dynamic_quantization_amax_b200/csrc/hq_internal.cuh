@@ -1,5 +1,6 @@
 // hq_internal.cuh -- declarations shared by the translation units of
-// libhq.so (api.cu, quantize.cu, gemm.cu, gemm_bs.cu, noalloc.cu, probe.cu).
+// libhq.so (api.cu, quantize.cu, gemm.cu, gemm_bs.cu, grad_bias.cu, norm.cu,
+// act_bwd.cu, noalloc.cu, probe.cu).
 // Not part of the public ABI.
 #pragma once
 
@@ -69,6 +70,68 @@ cudaError_t launch_grad_bias(const void* g, int xt, int64_t rows, int64_t cols, 
 cudaError_t launch_dequantize_blockwise(const uint8_t* q, int fmt, int64_t rows, int64_t cols, int64_t block,
                                         const float* scales, bool bf16_out, void* out, cudaStream_t stream);
 
+// RMS norm of h = x (+ residual) with FP8 output (norm.cu).  Element types:
+// 0 f32, 1 bf16, 2 f16.
+struct NormArgs {
+  const void* x;
+  int xt;
+  const void* residual;   // nullable
+  const void* weight;
+  int wt;
+  int64_t rows, cols;
+  float eps;
+  int fmt;
+  int64_t block;          // columns per scale; 0: one scale per row
+  uint8_t* q;
+  float* scales;          // [rows, nb]
+  void* residual_out;     // nullable; may be x or residual itself
+  void* y_out;            // nullable
+  float* rstd_out;        // nullable
+  cudaStream_t stream;
+};
+constexpr int64_t kNormMaxCols = 32768;
+cudaError_t launch_rmsnorm(const NormArgs& a);
+
+// Its backward pass: dx and, with dweight, the gain's gradient through
+// per-CTA partial sums in ws (contents on entry do not matter).
+struct NormBwdArgs {
+  const void* dy;
+  const void* h;
+  int xt;
+  const void* dres;       // nullable
+  const void* weight;
+  int wt;
+  const float* rstd;
+  int64_t rows, cols;
+  void* dx;
+  void* dweight;          // nullable, element type wt
+  float* ws;
+  cudaStream_t stream;
+};
+size_t rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a);
+
+// Activation backward from a block-wise FP8 checkpoint (act_bwd.cu).
+struct ActBwdArgs {
+  const void* g;
+  int gt;
+  const uint8_t* z_q;
+  int fmt;
+  int64_t block;
+  const float* z_scales;
+  int act;
+  int64_t rows, cols;
+  void* dz;               // may be g itself
+  void* dbias;            // nullable, element type gt
+  float* ws;
+  cudaStream_t stream;
+};
+// out[c] (element type ot) = sum over b of part[b, c] in f32, in a fixed order
+// (norm.cu); parts == 0 writes zeros.
+cudaError_t launch_column_partials(const float* part, int parts, int cols, void* out, int ot, cudaStream_t stream);
+size_t act_backward_workspace_bytes(int64_t rows, int64_t cols);
+cudaError_t launch_act_backward(const ActBwdArgs& a);
+
 struct GemmArgs {
   int kind;                 // 0: fp8 a8w8 (kind::f8f6f4), 1: bf16 (kind::f16)
   int fmt;                  // fp8 format of both operands (kind 0)
@@ -93,6 +156,14 @@ struct GemmArgs {
   int ring_len = 0, ring_idx = 0, ring_margin = 0;
   uint32_t* q_ws = nullptr;     // amax accumulator word (zero between calls)
   float* q_bscales = nullptr;   // set: q_out holds block-wise codes (32-column blocks, no ring), scales [M, N/32]
+  // activation epilogue (dense a8w8 only): out = bf16(act(z) + residual),
+  // z = acc * scales + bias, and z as block-wise FP8 (32-column blocks)
+  bool act_epilogue = false;
+  int act = 0;                    // hq_activation
+  const void* residual = nullptr; // bf16 [M, N]; may be out itself
+  uint8_t* z_q = nullptr;         // codes [M, N]
+  int z_fmt = 0;
+  float* z_scales = nullptr;      // [M, N / 32]
 };
 
 // Returns cudaSuccess or the failing call's error; *msg gets a description.

@@ -460,6 +460,161 @@ hq_status hq_gemm_a8w8_blockq(const uint8_t* xq, const uint8_t* wq, hq_fp8_forma
                               int64_t M, int64_t N, int64_t K, uint8_t* q_out, hq_fp8_format q_fmt, int64_t block,
                               float* q_scales, hq_stream_t stream);
 
+/* Activations of hq_gemm_a8w8_act and hq_act_backward_fp8:
+     HQ_ACT_RELU       max(z, 0); derivative 0 at 0
+     HQ_ACT_GELU       z Phi(z), Phi the standard normal distribution (erf form)
+     HQ_ACT_GELU_TANH  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+     HQ_ACT_SILU       z / (1 + e^-z) */
+typedef enum { HQ_ACT_NONE = 0, HQ_ACT_RELU = 1, HQ_ACT_GELU = 2, HQ_ACT_GELU_TANH = 3, HQ_ACT_SILU = 4 } hq_activation;
+
+/*
+ * The scaled FP8 GEMM with bias, activation and residual in its epilogue,
+ * and the 8-bit checkpoint of what the activation was applied to (the
+ * library's addition: the pages' linear_forward_fp8 stops at the bias, and
+ * their activation compression saves 8-bit tensors for the backward pass):
+ *
+ *   z[m, n]   = acc[m, n] * (x_scale[m'] * w_scale[n']) + bias[n]     (f32)
+ *   out[m, n] = bf16_rn( act(z[m, n]) + residual[m, n] )
+ *
+ * z stays in f32 through the activation and the residual addition; out is
+ * rounded once.  With z_q, z is also stored as block-wise FP8, 32 columns of
+ * a row to a scale: m = fmax / max |z| over the block's finite values (1
+ * when that is 0 or the quotient is not finite), z_q = saturating RNE code
+ * of z * m (NaN -> 0x7F), z_scales[m, n / 32] = 1/m -- the layout of
+ * hq_quantize_fp8_blockwise with block 32, quantized from f32 and not from
+ * a bf16 rounding of z.  hq_act_backward_fp8 reads it.
+ *
+ * Arguments as hq_gemm_a8w8, and:
+ *   bias      device bf16 [N], 4-byte aligned, or NULL
+ *   act       the activation; HQ_ACT_NONE leaves z as it is
+ *   residual  device bf16 [M, N], 16-byte aligned, or NULL; may be out
+ *             itself (the residual stream updated in place)
+ *   z_q       device uint8 [M, N], 16-byte aligned, or NULL: no checkpoint
+ *   z_fmt     format of the checkpoint's codes
+ *   z_block   32 with z_q (the only supported value); N % 32 == 0 then
+ *   z_scales  device f32 [M, N / 32], 4-byte aligned; given with z_q only
+ * M == 0 or N == 0 returns HQ_OK with no launch (out may be NULL then);
+ * K == 0 takes acc = 0.
+ * Errors: those of hq_gemm_a8w8, plus HQ_ERR_INVALID_ARG (bad act, z_q
+ *   without z_scales or the reverse, bad z_fmt, z_block or N with z_q),
+ *   HQ_ERR_MISALIGNED (bias, residual, z_q, z_scales) and HQ_ERR_OVERLAP
+ *   among all buffers (out equal to residual excepted).
+ */
+hq_status hq_gemm_a8w8_act(const uint8_t* xq, const uint8_t* wq, hq_fp8_format fmt, const float* x_scale,
+                           int64_t x_scale_len, const float* w_scale, int64_t w_scale_len, const void* bias,
+                           hq_activation act, const void* residual, int64_t M, int64_t N, int64_t K, void* out,
+                           uint8_t* z_q, hq_fp8_format z_fmt, int64_t z_block, float* z_scales, hq_stream_t stream);
+
+/*
+ * Backward pass of an activation from its 8-bit checkpoint, with the bias
+ * gradient of the layer that z belongs to (the library's addition, beside
+ * hq_grad_bias and the block-wise dequantize that it stands in for):
+ *   z      = f32(dec(z_q[r, c]) * z_scales[r, c / z_block])
+ *   dz     = g * act'(z)                    (f32, rounded once to g's dtype)
+ *   dbias  = sum over r of dz[r, c]         (of the unrounded f32 dz, summed
+ *            in f32 in a fixed order, rounded once to g's dtype)
+ * Calls with the same inputs give the same bits.  A checkpoint value of NaN
+ * gives dz = NaN; g's Inf and NaN propagate as in the f32 product.
+ *
+ * Arguments:
+ *   g          device [rows, cols] row-major, f32 / bf16 / f16 (gt): the
+ *              gradient of the activation's result, 16-byte aligned
+ *   z_q        device uint8 [rows, cols], 16-byte aligned; cols % 16 == 0
+ *   z_block    columns per scale, a positive multiple of 16 (32 for a
+ *              checkpoint of hq_gemm_a8w8_act)
+ *   z_scales   device f32 [rows, ceil(cols / z_block)]
+ *   act        the activation; HQ_ACT_NONE is refused (dz would be g)
+ *   dz         device [rows, cols] of gt, 16-byte aligned; may be g itself
+ *   dbias      device [cols] of gt, or NULL
+ *   workspace  with dbias: device, >= hq_act_backward_workspace_bytes bytes,
+ *              256-byte aligned; its contents on entry do not matter, and
+ *              calls that may run at the same time need one each
+ * rows == 0 writes dbias = 0; cols == 0 is a no-op.
+ * Errors: HQ_ERR_INVALID_ARG, HQ_ERR_MISALIGNED, HQ_ERR_OVERLAP (dz equal
+ *   to g excepted), HQ_ERR_WRONG_DEVICE, HQ_ERR_UNSUPPORTED_ARCH,
+ *   HQ_ERR_TOO_LARGE (rows or cols >= 2^31, rows * cols >= 2^40),
+ *   HQ_ERR_CUDA.
+ */
+size_t hq_act_backward_workspace_bytes(int64_t rows, int64_t cols);
+hq_status hq_act_backward_fp8(const void* g, hq_dtype gt, const uint8_t* z_q, hq_fp8_format z_fmt, int64_t z_block,
+                              const float* z_scales, hq_activation act, int64_t rows, int64_t cols, void* dz, void* dbias,
+                              void* workspace, size_t workspace_bytes, hq_stream_t stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and FP8 output (the
+ * library's addition: the step ahead of an FP8 GEMM in one pass over the
+ * data):
+ *   h      = x + residual                                  (f32; x alone without)
+ *   rstd   = 1 / sqrt( mean over the row of h^2 + eps )
+ *   y      = h * weight * rstd                             (f32)
+ *   q, scales: y quantized per row (block == 0) or per block of `block`
+ *          consecutive columns, the rules of hq_quantize_fp8 per token and
+ *          of hq_quantize_fp8_blockwise: amax over the finite |y|,
+ *          m = fmax / amax (1 when that is 0 or not finite), saturating RNE
+ *          codes of y * m (NaN -> 0x7F), scales = 1/m
+ * y is quantized from f32 and rounded once.  The norm is taken of the f32
+ * sum; residual_out receives that sum rounded to x's dtype.  A row with an
+ * infinity or NaN gives the formula's values; |h| above about 1e19
+ * overflows the f32 sum of squares (rstd = 0).
+ *
+ * Arguments:
+ *   x             device [rows, cols] row-major, f32 / bf16 / f16 (xt);
+ *                 cols up to 32768
+ *   residual      device [rows, cols] of xt, or NULL
+ *   weight        device [cols], f32 / bf16 / f16 (wt)
+ *   eps           in [1e-30, 1e30]
+ *   block         0: one scale per row; else a positive multiple of 16, with
+ *                 cols % 16 == 0
+ *   q             device uint8 [rows, cols]
+ *   scales        device f32 [rows] (block == 0) or [rows, ceil(cols / block)]
+ *   residual_out  device [rows, cols] of xt or NULL; only with residual; may
+ *                 be x or residual itself
+ *   y_out         device [rows, cols] of xt or NULL: y rounded to x's dtype
+ *   rstd_out      device f32 [rows] or NULL (the backward pass reads it)
+ *   Every buffer is aligned to its element size; where all rows also start
+ *   on 16-byte boundaries (weight and q likewise) the vector path runs.
+ * rows == 0 or cols == 0 returns HQ_OK with no launch.
+ * Errors: HQ_ERR_INVALID_ARG, HQ_ERR_MISALIGNED, HQ_ERR_OVERLAP
+ *   (residual_out equal to x or residual excepted), HQ_ERR_WRONG_DEVICE,
+ *   HQ_ERR_UNSUPPORTED_ARCH, HQ_ERR_TOO_LARGE, HQ_ERR_CUDA.
+ */
+hq_status hq_rmsnorm_fp8(const void* x, hq_dtype xt, const void* residual, const void* weight, hq_dtype wt,
+                         int64_t rows, int64_t cols, float eps, hq_fp8_format fmt, int64_t block, uint8_t* q,
+                         float* scales, void* residual_out, void* y_out, float* rstd_out, hq_stream_t stream);
+
+/*
+ * Backward pass of hq_rmsnorm_fp8's norm (the quantize passes the gradient
+ * through unchanged):
+ *   xh      = h * rstd,  gw = dy * weight
+ *   dx      = dres + rstd * (gw - xh * mean over the row of (gw * xh))
+ *   dweight = sum over the rows of dy * xh   (f32, in a fixed order, rounded
+ *             once to the weight's dtype)
+ * dx is the gradient of both x and residual.  Calls with the same inputs
+ * give the same bits.
+ *
+ * Arguments:
+ *   dy         device [rows, cols] of xt: the gradient of y; cols up to 32768
+ *   h          device [rows, cols] of xt: residual_out of the forward call
+ *              (x where it had no residual)
+ *   dres       device [rows, cols] of xt or NULL: the gradient that reaches
+ *              residual_out by other ways
+ *   weight     device [cols] of wt
+ *   rstd       device f32 [rows]: rstd_out of the forward call
+ *   dx         device [rows, cols] of xt, apart from every input
+ *   dweight    device [cols] of wt, or NULL (a fixed gain)
+ *   workspace  with dweight: device, >= hq_rmsnorm_backward_workspace_bytes
+ *              bytes, 256-byte aligned; its contents on entry do not matter,
+ *              and calls that may run at the same time need one each
+ * rows == 0 writes dweight = 0; cols == 0 is a no-op.
+ * Errors: HQ_ERR_INVALID_ARG, HQ_ERR_MISALIGNED, HQ_ERR_OVERLAP,
+ *   HQ_ERR_WRONG_DEVICE, HQ_ERR_UNSUPPORTED_ARCH, HQ_ERR_TOO_LARGE,
+ *   HQ_ERR_CUDA.
+ */
+size_t hq_rmsnorm_backward_workspace_bytes(int64_t rows, int64_t cols);
+hq_status hq_rmsnorm_backward(const void* dy, const void* h, hq_dtype xt, const void* dres, const void* weight,
+                              hq_dtype wt, const float* rstd, int64_t rows, int64_t cols, void* dx, void* dweight,
+                              void* workspace, size_t workspace_bytes, hq_stream_t stream);
+
 /*
  * Grouped (per-expert) scaled FP8 GEMM (megablocks-hip TODO-gg.md gmm):
  * for each expert e and each row r in [offsets[e], offsets[e+1]):
