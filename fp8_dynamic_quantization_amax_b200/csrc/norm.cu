@@ -17,6 +17,9 @@
 #include "fp8_cvt.cuh"
 #include "hq_internal.cuh"
 #include "launch.cuh"
+#include "ptx.cuh"
+
+#include <atomic>
 
 namespace hq {
 namespace {
@@ -151,6 +154,251 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(const NormParams p)
   }
 }
 
+// ------------------------------------------------------- 16-byte rows
+// A CTA takes rows blockIdx.x, + gridDim.x, ...; bulk copies (TMA) bring the
+// next rows of x and residual into a ring of shared-memory stages, thread t
+// holds E elements of the row (16-byte vectors t, t + T, ..) and its share
+// of the weight in registers.  One block barrier per row joins the sum of
+// squares and the maximum; behind it every thread has read the row's stage,
+// so the refill needs no barrier of its own.
+//
+// Block-wise scales: a block of 16-byte vectors that is a power of two up to
+// 32 lies inside one warp's consecutive lanes, so its maximum is a shuffle.
+constexpr int kRingStages = 8;
+constexpr int kRingMaxThreads = 1024;
+
+template <int XT>
+constexpr int vec_elems() {
+  return XT == 0 ? 4 : 8;
+}
+
+struct RingShared {
+  uint64_t full[kRingStages];
+  float sum[2][32];       // by row parity, per warp
+  uint32_t top[2][32];
+  int abort_flag;
+};
+
+__device__ __forceinline__ void ring_init(RingShared& sh, int stages) {
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < stages; ++s) ptx::mbar_init(&sh.full[s], 1);
+    sh.abort_flag = 0;
+    ptx::fence_mbarrier_init();
+  }
+  __syncthreads();
+}
+
+// After a wait that gave up: the copies still in flight into this CTA's
+// shared memory land (or the drain limit passes) before the CTA leaves.
+__device__ __forceinline__ void ring_drain(RingShared& sh, int stages, int64_t issued) {
+  if (threadIdx.x == 0) {
+    int dummy = 0;
+    for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
+      ptx::mbar_wait(&sh.full[i % stages], static_cast<uint32_t>((i / stages) & 1), &dummy, nullptr, 0, ptx::kDrainLimitNs);
+  }
+  __syncthreads();
+}
+
+// this warp's lanes' values joined over all warps of the CTA (after the barrier)
+__device__ __forceinline__ float join_sum(const float* red, int warps) {
+  const int lane = threadIdx.x & 31;
+  return warp_sum(lane < warps ? red[lane] : 0.0f);
+}
+__device__ __forceinline__ uint32_t join_max(const uint32_t* red, int warps) {
+  const int lane = threadIdx.x & 31;
+  return __reduce_max_sync(0xFFFFFFFFu, lane < warps ? red[lane] : 0u);
+}
+
+// VEC weights from column c as f32 (16-byte aligned weight, c a multiple of VEC)
+template <int VEC>
+__device__ __forceinline__ void load_weight(const void* w, int wt, int c, float* f) {
+  if (wt == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC; j += 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + j));
+      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
+    }
+  } else {
+    uint4 u = make_uint4(0, 0, 0, 0);
+    const unsigned short* ws = static_cast<const unsigned short*>(w) + c;
+    if (VEC == 8) {
+      u = __ldg(reinterpret_cast<const uint4*>(ws));
+    } else {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(ws));
+      u.x = v.x; u.y = v.y;
+    }
+    float t[8];
+    if (wt == 1) vec_widen<1>(u, t);
+    else vec_widen<2>(u, t);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) f[j] = t[j];
+  }
+}
+
+// VEC codes of y * m; EXACT: y may hold NaN
+template <int VEC, int FMT, bool EXACT>
+__device__ __forceinline__ void store_codes_as(uint8_t* q, const float2* y, float m) {
+  uint32_t c[VEC / 4];
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    const float2 t = f2_mul(y[j], make_float2(m, m));
+    const uint32_t c2 = EXACT ? cvt2_exact<FMT>(t.x, t.y) : cvt2_fast<FMT>(t.x, t.y);
+    c[j / 2] = (j & 1) ? (c[j / 2] | (c2 << 16)) : c2;
+  }
+  if (VEC == 8) *reinterpret_cast<uint2*>(q) = make_uint2(c[0], c[VEC / 4 - 1]);
+  else *reinterpret_cast<uint32_t*>(q) = c[0];
+}
+template <int VEC>
+__device__ __forceinline__ void store_codes(uint8_t* q, const float2* y, float m, int fmt, bool exact) {
+  if (exact) {
+    if (fmt == 0) store_codes_as<VEC, 0, true>(q, y, m);
+    else store_codes_as<VEC, 1, true>(q, y, m);
+  } else {
+    if (fmt == 0) store_codes_as<VEC, 0, false>(q, y, m);
+    else store_codes_as<VEC, 1, false>(q, y, m);
+  }
+}
+
+template <int XT, int E, bool RES>
+__global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormParams p, const int stages, unsigned* err) {
+  constexpr int VEC = vec_elems<XT>();
+  constexpr int ITEMS = E / VEC;
+  constexpr bool kWeightRegs = E <= 16;  // wider shares read the weight again per row (from L2)
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ RingShared sh;
+  const int tid = threadIdx.x, T = blockDim.x;
+  const int warp = tid >> 5, lane = tid & 31, warps = T >> 5;
+  const int nv = p.cols / VEC;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * elem_bytes<XT>();
+  const uint32_t stage_bytes = row_bytes * (RES ? 2 : 1);
+  ring_init(sh, stages);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t mine = (p.rows - 1 - static_cast<int64_t>(blockIdx.x)) / gridDim.x + 1;  // rows of this CTA (>= 1)
+  int64_t issued = 0;
+  auto issue = [&] {  // thread 0: the next row of this CTA into its stage
+    const int s = static_cast<int>(issued % stages);
+    const int64_t off = (blockIdx.x + issued * gridDim.x) * static_cast<int64_t>(row_bytes);
+    ptx::mbar_arrive_expect_tx(&sh.full[s], stage_bytes);
+    ptx::bulk_load(ring + s * stage_bytes, static_cast<const char*>(p.x) + off, row_bytes, &sh.full[s]);
+    if (RES)
+      ptx::bulk_load(ring + s * stage_bytes + row_bytes, static_cast<const char*>(p.residual) + off, row_bytes, &sh.full[s]);
+    ++issued;
+  };
+  if (tid == 0)
+    while (issued < mine && issued < stages) issue();
+  const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
+  float2 w[kWeightRegs ? E / 2 : 1];
+  if (kWeightRegs) {
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      if (v < nv)
+        load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(w + (kWeightRegs ? it * (VEC / 2) : 0)));
+    }
+  }
+  const int group = p.block ? p.block / VEC : 0;  // lanes per block
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int64_t i = 0; i < mine; ++i) {
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    const bool ok = ptx::mbar_wait(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
+    const uint4* xs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
+    const uint4* rs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
+    float2 h[E / 2];
+    float2 ss2 = make_float2(0.0f, 0.0f);
+    float vtop[ITEMS], top = 0.0f;
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      float2* hv = h + it * (VEC / 2);
+      vtop[it] = 0.0f;
+      if (v < nv) {
+        vec_widen<XT>(xs[v], reinterpret_cast<float*>(hv));
+        if (RES) {
+          float2 r[VEC / 2];
+          vec_widen<XT>(rs[v], reinterpret_cast<float*>(r));
+#pragma unroll
+          for (int j = 0; j < VEC / 2; ++j) hv[j] = f2_add(hv[j], r[j]);
+          if (p.residual_out)
+            vec_store(static_cast<char*>(p.residual_out) + row * row_bytes + static_cast<int64_t>(v) * 16,
+                      vec_narrow<XT>(reinterpret_cast<const float*>(hv)));
+        }
+        float2 wl[VEC / 2];
+        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          ss2 = f2_fma(hv[j], hv[j], ss2);
+          hv[j] = f2_mul(hv[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]);  // h w from here on
+          vtop[it] = max3_abs_nan(vtop[it], hv[j].x, hv[j].y);
+        }
+        top = max3_abs_nan(top, vtop[it], 0.0f);
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) hv[j] = make_float2(0.0f, 0.0f);
+      }
+    }
+    float ss = warp_sum(ss2.x + ss2.y);
+    const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));  // NaN's bits are above infinity's
+    const int par = static_cast<int>(i & 1);
+    if (lane == 0) {
+      sh.sum[par][warp] = ss;
+      sh.top[par][warp] = wtop;
+    }
+    if (__syncthreads_or(!ok)) break;  // the whole CTA agrees on giving up
+    if (tid == 0 && issued < mine) issue();
+    ss = join_sum(sh.sum[par], warps);
+    const uint32_t tbits = join_max(sh.top[par], warps);
+    const float rstd = rsqrtf(fmaf(ss, inv_cols, p.eps));
+    float amax = __fmul_rn(__uint_as_float(tbits), rstd);
+    const bool special = tbits >= kInfBits || !(amax <= FLT_MAX);
+#pragma unroll
+    for (int e = 0; e < E / 2; ++e) h[e] = f2_mul(h[e], make_float2(rstd, rstd));  // y
+    if (special) {  // amax over the finite |y| alone
+      float fin = 0.0f;
+#pragma unroll
+      for (int it = 0; it < ITEMS; ++it) {
+        float vt = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+          vt = fmaxf(vt, fmaxf(finite_abs(h[it * (VEC / 2) + j].x), finite_abs(h[it * (VEC / 2) + j].y)));
+        vtop[it] = vt;
+        fin = fmaxf(fin, vt);
+      }
+      const uint32_t wfin = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fin));
+      __syncthreads();  // everyone has read this row's maxima
+      if (lane == 0) sh.top[par][warp] = wfin;
+      __syncthreads();
+      amax = __uint_as_float(join_max(sh.top[par], warps));
+    }
+    if (tid == 0 && p.rstd_out) p.rstd_out[row] = rstd;
+    float m = 1.0f;
+    if (group == 0) {
+      m = multiplier_of(amax, p.fmt);
+      if (tid == 0) p.scales[row] = __fdiv_rn(1.0f, m);
+    }
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      if (group != 0) {
+        float bt = vtop[it];
+        for (int o = 1; o < group; o <<= 1) bt = fmaxf(bt, __shfl_xor_sync(0xFFFFFFFFu, bt, o));
+        m = multiplier_of(special ? bt : __fmul_rn(bt, rstd), p.fmt);
+        if (v < nv && (lane & (group - 1)) == 0) p.scales[row * p.nb + v / group] = __fdiv_rn(1.0f, m);
+      }
+      if (v < nv) {
+        const int64_t at = row * p.cols + static_cast<int64_t>(v) * VEC;
+        const float2* y = h + it * (VEC / 2);
+        if (p.y_out)
+          vec_store(static_cast<char*>(p.y_out) + at * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(y)));
+        store_codes<VEC>(p.q + at, y, m, p.fmt, special);
+      }
+    }
+    if (++stage == stages) { stage = 0; phase ^= 1u; }
+  }
+  if (sh.abort_flag) ring_drain(sh, stages, issued);
+}
+
 struct NormBwdParams {
   const void* dy;
   const void* h;
@@ -198,6 +446,126 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(const NormBwdPa
     for (int c = tid; c < p.cols; c += kAnyThreads) p.part[static_cast<int64_t>(blockIdx.x) * p.cols + c] = dw[c];
 }
 
+// 16-byte rows: the forward kernel's ring over dy, h and dres.  Both passes
+// over a row (the mean, then dx and dw) read its stage, so the stage of row
+// i is refilled after row i + 1's barrier.  dw stays in registers.
+template <int XT, int E, bool DRES>
+__global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_bwd_ring(const NormBwdParams p, const int stages, unsigned* err) {
+  constexpr int VEC = vec_elems<XT>();
+  constexpr int ITEMS = E / VEC;
+  constexpr bool kWeightRegs = E <= 16;
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ RingShared sh;
+  const int tid = threadIdx.x, T = blockDim.x;
+  const int warp = tid >> 5, lane = tid & 31, warps = T >> 5;
+  const int nv = p.cols / VEC;
+  const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * elem_bytes<XT>();
+  const uint32_t stage_bytes = row_bytes * (DRES ? 3 : 2);
+  ring_init(sh, stages);
+  pdl_wait();
+  pdl_launch_dependents();
+  const int64_t mine = (p.rows - 1 - static_cast<int64_t>(blockIdx.x)) / gridDim.x + 1;
+  int64_t issued = 0;
+  auto issue = [&] {
+    const int s = static_cast<int>(issued % stages);
+    const int64_t off = (blockIdx.x + issued * gridDim.x) * static_cast<int64_t>(row_bytes);
+    uint8_t* to = ring + s * stage_bytes;
+    ptx::mbar_arrive_expect_tx(&sh.full[s], stage_bytes);
+    ptx::bulk_load(to, static_cast<const char*>(p.dy) + off, row_bytes, &sh.full[s]);
+    ptx::bulk_load(to + row_bytes, static_cast<const char*>(p.h) + off, row_bytes, &sh.full[s]);
+    if (DRES) ptx::bulk_load(to + 2 * row_bytes, static_cast<const char*>(p.dres) + off, row_bytes, &sh.full[s]);
+    ++issued;
+  };
+  if (tid == 0)
+    while (issued < mine && issued < stages) issue();
+  const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
+  float2 w[kWeightRegs ? E / 2 : 1], dw[E / 2];
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) {
+    const int v = it * T + tid;
+    if (kWeightRegs && v < nv)
+      load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(w + (kWeightRegs ? it * (VEC / 2) : 0)));
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) dw[it * (VEC / 2) + j] = make_float2(0.0f, 0.0f);
+  }
+  int stage = 0;
+  uint32_t phase = 0;
+  for (int64_t i = 0; i < mine; ++i) {
+    const int64_t row = blockIdx.x + i * gridDim.x;
+    const float rs = __ldg(p.rstd + row);
+    const bool ok = ptx::mbar_wait(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
+    const uint4* gs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
+    const uint4* hs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
+    const uint4* ds = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 2 * row_bytes);
+    const float2 rs2 = make_float2(rs, rs);
+    float2 dot2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      if (v < nv) {
+        float2 g[VEC / 2], h[VEC / 2], wl[VEC / 2];
+        vec_widen<XT>(gs[v], reinterpret_cast<float*>(g));
+        vec_widen<XT>(hs[v], reinterpret_cast<float*>(h));
+        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j)
+          dot2 = f2_fma(f2_mul(g[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]), h[j], dot2);
+      }
+    }
+    const float dot = warp_sum(dot2.x + dot2.y);
+    const int par = static_cast<int>(i & 1);
+    if (lane == 0) sh.sum[par][warp] = dot;
+    if (__syncthreads_or(!ok)) break;
+    // behind this barrier nobody reads the previous row's stage any more
+    if (tid == 0 && i > 0 && stages > 1 && issued < mine) issue();
+    const float mean = -rs * (join_sum(sh.sum[par], warps) * inv_cols);
+    const float2 mean2 = make_float2(mean, mean);  // -mean(gw xh)
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      if (v < nv) {
+        float2 g[VEC / 2], h[VEC / 2], d[VEC / 2], wl[VEC / 2];
+        vec_widen<XT>(gs[v], reinterpret_cast<float*>(g));
+        vec_widen<XT>(hs[v], reinterpret_cast<float*>(h));
+        if (DRES) vec_widen<XT>(ds[v], reinterpret_cast<float*>(d));
+        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
+#pragma unroll
+        for (int j = 0; j < VEC / 2; ++j) {
+          const float2 xh = f2_mul(h[j], rs2);
+          const float2 gw = f2_mul(g[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]);
+          dw[it * (VEC / 2) + j] = f2_fma(g[j], xh, dw[it * (VEC / 2) + j]);
+          const float2 t = f2_fma(xh, mean2, gw);
+          d[j] = DRES ? f2_fma(t, rs2, d[j]) : f2_mul(t, rs2);
+        }
+        vec_store(static_cast<char*>(p.dx) + row * row_bytes + static_cast<int64_t>(v) * 16,
+                  vec_narrow<XT>(reinterpret_cast<const float*>(d)));
+      }
+    }
+    if (stages == 1) {  // rows so wide that one fits: it is refilled once both passes are through
+      __syncthreads();
+      if (tid == 0 && issued < mine) issue();
+    }
+    if (++stage == stages) { stage = 0; phase ^= 1u; }
+  }
+  if (sh.abort_flag) {
+    ring_drain(sh, stages, issued);
+    return;
+  }
+  if (p.part == nullptr) return;
+#pragma unroll
+  for (int it = 0; it < ITEMS; ++it) {
+    const int v = it * T + tid;
+    if (v < nv) {
+      float* to = p.part + static_cast<int64_t>(blockIdx.x) * p.cols + static_cast<int64_t>(v) * VEC;
+#pragma unroll
+      for (int j = 0; j < VEC / 2; j += 2) {
+        const float2 a = dw[it * (VEC / 2) + j], b = dw[it * (VEC / 2) + j + 1];
+        *reinterpret_cast<float4*>(to + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
+      }
+    }
+  }
+}
+
 // dweight[c] = sum of the partials of column c.  A CTA takes 32 columns, its
 // warp w the w-th eighth of the partial rows; the eighths join in order.
 constexpr int kDwWarps = 8;
@@ -229,16 +597,105 @@ int sm_count() {
   return device_sm_count(dev);
 }
 
+// Opens up to kRingSmem of dynamic shared memory to a ring kernel, once per
+// device.
+constexpr int kRingSmem = 224 * 1024;
+template <typename K>
+cudaError_t open_smem(K kernel, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingSmem);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+// Launch shape of a ring kernel: E elements per thread, T threads, S stages
+// of stage_bytes.  64 registers a thread let 1024 / T CTAs share an SM, and
+// they share its shared memory.
+struct RingShape {
+  int threads, ctas, stages;
+};
+RingShape ring_shape(int64_t cols, int e, int64_t stage_bytes, int min_stages) {
+  RingShape r;
+  r.threads = static_cast<int>((((cols + e - 1) / e) + 31) / 32 * 32);
+  r.ctas = kRingMaxThreads / r.threads;
+  if (r.ctas > 16) r.ctas = 16;
+  while (r.ctas > 1 && (kRingSmem / r.ctas - 1024) / stage_bytes < min_stages) --r.ctas;
+  const int64_t s = (kRingSmem / r.ctas - 1024) / stage_bytes;
+  r.stages = static_cast<int>(s > kRingStages ? kRingStages : s);
+  return r;
+}
+
+template <int XT, int E, bool RES>
+cudaError_t norm_ring(const NormArgs& a, const NormParams& p) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = open_smem(k_rmsnorm_ring<XT, E, RES>, done);
+  if (e != cudaSuccess) return e;
+  const int64_t stage = a.cols * elem_bytes<XT>() * (RES ? 2 : 1);
+  const RingShape r = ring_shape(a.cols, E, stage, 2);
+  const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
+  const int64_t grid = a.rows < most ? a.rows : most;
+  const int64_t per = (a.rows + grid - 1) / grid;
+  const int stages = static_cast<int>(per < r.stages ? per : r.stages);
+  return launch_pdl(k_rmsnorm_ring<XT, E, RES>, dim3(static_cast<unsigned>(grid)), dim3(r.threads),
+                    static_cast<size_t>(stages * stage), a.stream, false, p, stages, device_error_word());
+}
+
 template <int XT>
 cudaError_t norm_run(const NormArgs& a, const NormParams& p) {
+  constexpr int VEC = vec_elems<XT>();
+  const int group = p.block / VEC;
+  const bool ring = a.cols % VEC == 0 && aligned16(a.x) && aligned16(a.residual) && aligned16(a.residual_out) &&
+                    aligned16(a.y_out) && aligned16(a.weight) && reinterpret_cast<uintptr_t>(a.q) % VEC == 0 &&
+                    (p.block == 0 || (group <= 32 && (group & (group - 1)) == 0)) &&
+                    a.cols * elem_bytes<XT>() * (a.residual ? 2 : 1) <= kRingSmem - 1024;
+  if (ring) {
+    // 8 elements a thread where a CTA has one row (latency), 16 up to 16384
+    // columns, 32 beyond
+    if (a.rows <= sm_count() && a.cols <= 8 * kRingMaxThreads)
+      return a.residual ? norm_ring<XT, 8, true>(a, p) : norm_ring<XT, 8, false>(a, p);
+    if (a.cols <= 16 * kRingMaxThreads)
+      return a.residual ? norm_ring<XT, 16, true>(a, p) : norm_ring<XT, 16, false>(a, p);
+    return a.residual ? norm_ring<XT, 32, true>(a, p) : norm_ring<XT, 32, false>(a, p);
+  }
   const int64_t grid = a.rows < 8 * sm_count() ? a.rows : 8 * sm_count();
   return launch_pdl(k_rmsnorm_any<XT>, dim3(static_cast<unsigned>(grid)), dim3(kAnyThreads), 0, a.stream, false, p);
 }
 
 int64_t bwd_parts(int64_t rows) { return rows < kBwdParts ? rows : kBwdParts; }
 
+template <int XT, int E, bool DRES>
+cudaError_t bwd_ring(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = open_smem(k_rmsnorm_bwd_ring<XT, E, DRES>, done);
+  if (e != cudaSuccess) return e;
+  const int64_t stage = a.cols * elem_bytes<XT>() * (DRES ? 3 : 2);
+  const RingShape r = ring_shape(a.cols, E, stage, 2);
+  const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
+  if (grid > most) grid = most;
+  const int64_t per = (a.rows + grid - 1) / grid;
+  const int stages = static_cast<int>(per < r.stages ? per : r.stages);
+  return launch_pdl(k_rmsnorm_bwd_ring<XT, E, DRES>, dim3(static_cast<unsigned>(grid)), dim3(r.threads),
+                    static_cast<size_t>(stages * stage), a.stream, false, p, stages, device_error_word());
+}
+
+// grid: the largest number of CTAs (and partial rows); the number launched.
 template <int XT>
-cudaError_t bwd_run(const NormBwdArgs& a, const NormBwdParams& p, int64_t grid) {
+cudaError_t bwd_run(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
+  constexpr int VEC = vec_elems<XT>();
+  const int64_t stage = a.cols * elem_bytes<XT>() * (a.dres ? 3 : 2);
+  const bool ring = a.cols % VEC == 0 && aligned16(a.dy) && aligned16(a.h) && aligned16(a.dres) && aligned16(a.dx) &&
+                    aligned16(a.weight) && stage <= kRingSmem - 1024;
+  if (ring) {
+    if (a.cols <= 16 * kRingMaxThreads)
+      return a.dres ? bwd_ring<XT, 16, true>(a, p, grid) : bwd_ring<XT, 16, false>(a, p, grid);
+    return a.dres ? bwd_ring<XT, 32, true>(a, p, grid) : bwd_ring<XT, 32, false>(a, p, grid);
+  }
   const size_t smem = p.part ? static_cast<size_t>(a.cols) * 4 : 0;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd_any<XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -254,9 +711,9 @@ cudaError_t launch_rmsnorm(const NormArgs& a) {
   NormParams p;
   p.x = a.x; p.residual = a.residual; p.weight = a.weight; p.wt = a.wt;
   p.rows = static_cast<int>(a.rows); p.cols = static_cast<int>(a.cols); p.eps = a.eps; p.fmt = a.fmt;
-  // a block wider than the row is the row
-  p.block = static_cast<int>(a.block);
-  p.nb = a.block ? static_cast<int>((a.cols + a.block - 1) / a.block) : 0;
+  // a block as wide as the row is the row: the same scale at the same place
+  p.block = a.block >= a.cols ? 0 : static_cast<int>(a.block);
+  p.nb = p.block ? static_cast<int>((a.cols + p.block - 1) / p.block) : 0;
   p.q = a.q; p.scales = a.scales; p.residual_out = a.residual_out; p.y_out = a.y_out; p.rstd_out = a.rstd_out;
   if (a.xt == 0) return norm_run<0>(a, p);
   if (a.xt == 1) return norm_run<1>(a, p);
@@ -272,7 +729,7 @@ cudaError_t launch_rmsnorm_backward(const NormBwdArgs& a) {
   p.dy = a.dy; p.h = a.h; p.dres = a.dres; p.weight = a.weight; p.wt = a.wt; p.rstd = a.rstd;
   p.rows = static_cast<int>(a.rows); p.cols = static_cast<int>(a.cols); p.dx = a.dx;
   p.part = a.dweight ? a.ws : nullptr;
-  const int64_t parts = bwd_parts(a.rows);
+  int64_t parts = bwd_parts(a.rows);
   cudaError_t e = cudaSuccess;
   if (a.rows > 0) {
     if (a.xt == 0) e = bwd_run<0>(a, p, parts);
