@@ -112,12 +112,14 @@ __device__ __forceinline__ uint4 vec_load(const void* p) {
   uint4 u;
   asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w)
-               : "l"(p)
-               : "memory");
+               : "l"(p));
   return u;
 }
+// No memory clobber: shared-memory loads of the next vector may move above it
+// (with one, each vector of a row waited for the one before).  Volatile asm
+// keeps its order among vec_load and vec_store.
 __device__ __forceinline__ void vec_store(void* p, const uint4& u) {
-  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w) : "memory");
+  asm volatile("st.global.v4.u32 [%0], {%1, %2, %3, %4};" ::"l"(p), "r"(u.x), "r"(u.y), "r"(u.z), "r"(u.w));
 }
 
 }  // namespace

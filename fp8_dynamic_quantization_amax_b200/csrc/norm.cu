@@ -165,7 +165,17 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(const NormParams p)
 // Block-wise scales: a block of 16-byte vectors that is a power of two up to
 // 32 lies inside one warp's consecutive lanes, so its maximum is a shuffle.
 constexpr int kRingStages = 8;
-constexpr int kRingMaxThreads = 1024;
+// Elements per thread.  Most rows run with 16 or 24 elements and the weight
+// in registers, up to 512 threads of 128 registers per SM: measured on
+// [16384, 8192] bf16 with a residual, 16 elements in one CTA of 512 threads
+// took 148 us, held to 64 registers with two CTAs 171 us (the compiler then
+// orders the loads behind one another), 32 elements in two CTAs of 256
+// threads 171 us, in one 190 us; the backward pass 158, 180, 165 and 164 us.
+// Eight elements serve a single row per CTA (latency) and narrow rows; rows
+// beyond 16384 columns hold 32 elements in up to 1024 threads and read the
+// weight per row.
+constexpr int kRingMaxCols = 16384;
+constexpr int ring_max_threads(int e, bool wide) { return (e == 8 || wide) ? 1024 : 512; }
 
 template <int XT>
 constexpr int vec_elems() {
@@ -188,15 +198,18 @@ __device__ __forceinline__ void ring_init(RingShared& sh, int stages) {
   __syncthreads();
 }
 
-// After a wait that gave up: the copies still in flight into this CTA's
-// shared memory land (or the drain limit passes) before the CTA leaves.
-__device__ __forceinline__ void ring_drain(RingShared& sh, int stages, int64_t issued) {
-  if (threadIdx.x == 0) {
-    int dummy = 0;
-    for (int64_t i = issued > stages ? issued - stages : 0; i < issued; ++i)
-      ptx::mbar_wait(&sh.full[i % stages], static_cast<uint32_t>((i / stages) & 1), &dummy, nullptr, 0, ptx::kDrainLimitNs);
-  }
-  __syncthreads();
+// After a wait that gave up at `stage` (of parity `phase`): the copies still
+// in flight into this CTA's shared memory land, or the drain limit passes,
+// before it leaves.  Stages from `stage` on, up to and without next_stage,
+// hold rows not yet waited for; where the two are equal, all of them may.
+// A stage that was never filled in this round has nothing in flight: its
+// wait ends at the limit.
+__device__ __forceinline__ void drain_stages(uint64_t* full, int stages, int stage, uint32_t phase, int next_stage) {
+  int dummy = 0;
+  do {
+    ptx::mbar_wait(&full[stage], phase, &dummy, nullptr, 0, ptx::kDrainLimitNs);
+    if (++stage == stages) { stage = 0; phase ^= 1u; }
+  } while (stage != next_stage);
 }
 
 // this warp's lanes' values joined over all warps of the CTA (after the barrier)
@@ -259,11 +272,11 @@ __device__ __forceinline__ void store_codes(uint8_t* q, const float2* y, float m
   }
 }
 
-template <int XT, int E, bool RES>
-__global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormParams p, const int stages, unsigned* err) {
+template <int XT, int E, bool RES, bool WIDE>
+__global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(const NormParams p, const int stages, unsigned* err) {
   constexpr int VEC = vec_elems<XT>();
   constexpr int ITEMS = E / VEC;
-  constexpr bool kWeightRegs = E <= 16;  // wider shares read the weight again per row (from L2)
+  constexpr bool kWeightRegs = !WIDE;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ RingShared sh;
   const int tid = threadIdx.x, T = blockDim.x;
@@ -274,19 +287,21 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
   ring_init(sh, stages);
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t mine = (p.rows - 1 - static_cast<int64_t>(blockIdx.x)) / gridDim.x + 1;  // rows of this CTA (>= 1)
-  int64_t issued = 0;
-  auto issue = [&] {  // thread 0: the next row of this CTA into its stage
-    const int s = static_cast<int>(issued % stages);
-    const int64_t off = (blockIdx.x + issued * gridDim.x) * static_cast<int64_t>(row_bytes);
+  const int stride = static_cast<int>(gridDim.x);
+  int next = static_cast<int>(blockIdx.x);  // thread 0: the next row to bring in, and its stage
+  int next_stage = 0;
+  auto issue = [&] {
+    const int s = next_stage;
+    const int64_t off = static_cast<int64_t>(next) * row_bytes;
     ptx::mbar_arrive_expect_tx(&sh.full[s], stage_bytes);
     ptx::bulk_load(ring + s * stage_bytes, static_cast<const char*>(p.x) + off, row_bytes, &sh.full[s]);
     if (RES)
       ptx::bulk_load(ring + s * stage_bytes + row_bytes, static_cast<const char*>(p.residual) + off, row_bytes, &sh.full[s]);
-    ++issued;
+    next = p.rows - next > stride ? next + stride : p.rows;  // no overflow near 2^31 rows
+    if (++next_stage == stages) next_stage = 0;
   };
   if (tid == 0)
-    while (issued < mine && issued < stages) issue();
+    for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
   float2 w[kWeightRegs ? E / 2 : 1];
   if (kWeightRegs) {
@@ -297,14 +312,25 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
         load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(w + (kWeightRegs ? it * (VEC / 2) : 0)));
     }
   }
-  const int group = p.block ? p.block / VEC : 0;  // lanes per block
+  const int group = p.block ? p.block / VEC : 0;  // lanes per block, a power of two
+  const int group_log = 31 - __clz(group | 1);
   int stage = 0;
   uint32_t phase = 0;
-  for (int64_t i = 0; i < mine; ++i) {
-    const int64_t row = blockIdx.x + i * gridDim.x;
-    const bool ok = ptx::mbar_wait(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
+  int par = 0;
+  for (int row = static_cast<int>(blockIdx.x); row < p.rows; row = p.rows - row > stride ? row + stride : p.rows) {
+    const bool ok = ptx::mbar_wait_inline(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
     const uint4* xs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
     const uint4* rs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
+    // every vector is asked for before the first is used
+    uint4 xr[ITEMS], rr[RES ? ITEMS : 1];
+#pragma unroll
+    for (int it = 0; it < ITEMS; ++it) {
+      const int v = it * T + tid;
+      if (v < nv) {
+        xr[it] = xs[v];
+        if (RES) rr[RES ? it : 0] = rs[v];
+      }
+    }
     float2 h[E / 2];
     float2 ss2 = make_float2(0.0f, 0.0f);
     float vtop[ITEMS], top = 0.0f;
@@ -314,14 +340,14 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
       float2* hv = h + it * (VEC / 2);
       vtop[it] = 0.0f;
       if (v < nv) {
-        vec_widen<XT>(xs[v], reinterpret_cast<float*>(hv));
+        vec_widen<XT>(xr[it], reinterpret_cast<float*>(hv));
         if (RES) {
           float2 r[VEC / 2];
-          vec_widen<XT>(rs[v], reinterpret_cast<float*>(r));
+          vec_widen<XT>(rr[RES ? it : 0], reinterpret_cast<float*>(r));
 #pragma unroll
           for (int j = 0; j < VEC / 2; ++j) hv[j] = f2_add(hv[j], r[j]);
           if (p.residual_out)
-            vec_store(static_cast<char*>(p.residual_out) + row * row_bytes + static_cast<int64_t>(v) * 16,
+            vec_store(static_cast<char*>(p.residual_out) + static_cast<int64_t>(row) * row_bytes + v * 16,
                       vec_narrow<XT>(reinterpret_cast<const float*>(hv)));
         }
         float2 wl[VEC / 2];
@@ -340,13 +366,12 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
     }
     float ss = warp_sum(ss2.x + ss2.y);
     const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));  // NaN's bits are above infinity's
-    const int par = static_cast<int>(i & 1);
     if (lane == 0) {
       sh.sum[par][warp] = ss;
       sh.top[par][warp] = wtop;
     }
     if (__syncthreads_or(!ok)) break;  // the whole CTA agrees on giving up
-    if (tid == 0 && issued < mine) issue();
+    if (tid == 0 && next < p.rows) issue();
     ss = join_sum(sh.sum[par], warps);
     const uint32_t tbits = join_max(sh.top[par], warps);
     const float rstd = rsqrtf(fmaf(ss, inv_cols, p.eps));
@@ -384,10 +409,10 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
         float bt = vtop[it];
         for (int o = 1; o < group; o <<= 1) bt = fmaxf(bt, __shfl_xor_sync(0xFFFFFFFFu, bt, o));
         m = multiplier_of(special ? bt : __fmul_rn(bt, rstd), p.fmt);
-        if (v < nv && (lane & (group - 1)) == 0) p.scales[row * p.nb + v / group] = __fdiv_rn(1.0f, m);
+        if (v < nv && (lane & (group - 1)) == 0) p.scales[static_cast<int64_t>(row) * p.nb + (v >> group_log)] = __fdiv_rn(1.0f, m);
       }
       if (v < nv) {
-        const int64_t at = row * p.cols + static_cast<int64_t>(v) * VEC;
+        const int64_t at = static_cast<int64_t>(row) * p.cols + v * VEC;
         const float2* y = h + it * (VEC / 2);
         if (p.y_out)
           vec_store(static_cast<char*>(p.y_out) + at * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(y)));
@@ -395,8 +420,12 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_ring(const NormP
       }
     }
     if (++stage == stages) { stage = 0; phase ^= 1u; }
+    par ^= 1;
   }
-  if (sh.abort_flag) ring_drain(sh, stages, issued);
+  if (sh.abort_flag) {
+    if (tid == 0) drain_stages(sh.full, stages, stage, phase, next_stage);
+    __syncthreads();
+  }
 }
 
 struct NormBwdParams {
@@ -412,6 +441,7 @@ struct NormBwdParams {
 };
 
 constexpr int kBwdParts = 296;  // two CTAs per SM
+constexpr int kTeams = 15;      // teams of a backward CTA at most (barriers 1 .. 15)
 
 // CTA b takes rows b, b + grid, ...; dw sums in shared memory, one slot per
 // column, each touched by one thread only.
@@ -446,38 +476,70 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_bwd_any(const NormBwdPa
     for (int c = tid; c < p.cols; c += kAnyThreads) p.part[static_cast<int64_t>(blockIdx.x) * p.cols + c] = dw[c];
 }
 
-// 16-byte rows: the forward kernel's ring over dy, h and dres.  Both passes
-// over a row (the mean, then dx and dw) read its stage, so the stage of row
-// i is refilled after row i + 1's barrier.  dw stays in registers.
-template <int XT, int E, bool DRES>
-__global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_bwd_ring(const NormBwdParams p, const int stages, unsigned* err) {
+// Barrier of one team of T threads (a power of two of them share a CTA), and
+// whether any of its threads says so.
+__device__ __forceinline__ bool team_any(int team, int T, bool say) {
+  if (T == 32) return __any_sync(0xFFFFFFFFu, say);
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %3, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned p, %1, %2, q;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(team + 1), "r"(T), "r"(say ? 1u : 0u)
+      : "memory");
+  return r != 0;
+}
+
+// 16-byte rows: the forward kernel's ring over dy, h and dres.  A CTA is
+// `teams` teams of T threads with a row and a ring each (narrow rows: enough
+// rows in flight without a partial row of dw per row).  Both passes over a
+// row (the mean, then dx and dw) read its stage, so the stage of row i is
+// refilled after row i + 1's barrier.  dw stays in registers; the teams'
+// sums join in order through shared memory.
+template <int XT, int E, bool DRES, bool WIDE>
+__global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
+    k_rmsnorm_bwd_ring(const NormBwdParams p, const int teams, const int stages, unsigned* err) {
   constexpr int VEC = vec_elems<XT>();
   constexpr int ITEMS = E / VEC;
-  constexpr bool kWeightRegs = E <= 16;
-  extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ RingShared sh;
-  const int tid = threadIdx.x, T = blockDim.x;
-  const int warp = tid >> 5, lane = tid & 31, warps = T >> 5;
+  constexpr bool kWeightRegs = !WIDE;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ uint64_t full[kTeams][kRingStages];
+  __shared__ float sums[2][32];  // by row parity, per warp of the CTA
+  __shared__ int abort_flag;
+  const int T = blockDim.x / teams;
+  const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
+  const int lane = tid & 31, warps = T >> 5;
   const int nv = p.cols / VEC;
   const uint32_t row_bytes = static_cast<uint32_t>(p.cols) * elem_bytes<XT>();
   const uint32_t stage_bytes = row_bytes * (DRES ? 3 : 2);
-  ring_init(sh, stages);
+  uint8_t* ring = smem + team * stages * stage_bytes;
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) ptx::mbar_init(&full[team][s], 1);
+    if (team == 0) abort_flag = 0;
+    ptx::fence_mbarrier_init();
+  }
+  __syncthreads();
   pdl_wait();
   pdl_launch_dependents();
-  const int64_t mine = (p.rows - 1 - static_cast<int64_t>(blockIdx.x)) / gridDim.x + 1;
-  int64_t issued = 0;
+  // rows of this team: first, first + stride, .. (grid and teams are small: all in int)
+  const int first = static_cast<int>(blockIdx.x) * teams + team;
+  const int stride = static_cast<int>(gridDim.x) * teams;
+  int next = first;  // thread 0: the next row to bring in, and its stage
+  int next_stage = 0;
   auto issue = [&] {
-    const int s = static_cast<int>(issued % stages);
-    const int64_t off = (blockIdx.x + issued * gridDim.x) * static_cast<int64_t>(row_bytes);
+    const int s = next_stage;
+    const int64_t off = static_cast<int64_t>(next) * row_bytes;
     uint8_t* to = ring + s * stage_bytes;
-    ptx::mbar_arrive_expect_tx(&sh.full[s], stage_bytes);
-    ptx::bulk_load(to, static_cast<const char*>(p.dy) + off, row_bytes, &sh.full[s]);
-    ptx::bulk_load(to + row_bytes, static_cast<const char*>(p.h) + off, row_bytes, &sh.full[s]);
-    if (DRES) ptx::bulk_load(to + 2 * row_bytes, static_cast<const char*>(p.dres) + off, row_bytes, &sh.full[s]);
-    ++issued;
+    uint64_t* bar = &full[team][s];
+    ptx::mbar_arrive_expect_tx(bar, stage_bytes);
+    ptx::bulk_load(to, static_cast<const char*>(p.dy) + off, row_bytes, bar);
+    ptx::bulk_load(to + row_bytes, static_cast<const char*>(p.h) + off, row_bytes, bar);
+    if (DRES) ptx::bulk_load(to + 2 * row_bytes, static_cast<const char*>(p.dres) + off, row_bytes, bar);
+    next = p.rows - next > stride ? next + stride : p.rows;  // no overflow near 2^31 rows
+    if (++next_stage == stages) next_stage = 0;
   };
   if (tid == 0)
-    while (issued < mine && issued < stages) issue();
+    for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
   float2 w[kWeightRegs ? E / 2 : 1], dw[E / 2];
 #pragma unroll
@@ -488,12 +550,16 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_bwd_ring(const N
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) dw[it * (VEC / 2) + j] = make_float2(0.0f, 0.0f);
   }
+  float rs_next = first < p.rows ? __ldg(p.rstd + first) : 0.0f;
   int stage = 0;
   uint32_t phase = 0;
-  for (int64_t i = 0; i < mine; ++i) {
-    const int64_t row = blockIdx.x + i * gridDim.x;
-    const float rs = __ldg(p.rstd + row);
-    const bool ok = ptx::mbar_wait(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
+  bool ahead = false;  // a row of this team is done
+  int par = 0;
+  for (int row = first; row < p.rows;) {
+    const float rs = rs_next;
+    const int row_next = p.rows - row > stride ? row + stride : p.rows;
+    if (row_next < p.rows) rs_next = __ldg(p.rstd + row_next);
+    const bool ok = ptx::mbar_wait_inline(&full[team][stage], phase, &abort_flag, err, kDevErrTimeout);
     const uint4* gs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
     const uint4* hs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
     const uint4* ds = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 2 * row_bytes);
@@ -512,13 +578,14 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_bwd_ring(const N
           dot2 = f2_fma(f2_mul(g[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]), h[j], dot2);
       }
     }
-    const float dot = warp_sum(dot2.x + dot2.y);
-    const int par = static_cast<int>(i & 1);
-    if (lane == 0) sh.sum[par][warp] = dot;
-    if (__syncthreads_or(!ok)) break;
+    float dot = warp_sum(dot2.x + dot2.y);
+    if (lane == 0) sums[par][threadIdx.x >> 5] = dot;
+    if (team_any(team, T, !ok)) break;  // the team agrees on giving up
     // behind this barrier nobody reads the previous row's stage any more
-    if (tid == 0 && i > 0 && stages > 1 && issued < mine) issue();
-    const float mean = -rs * (join_sum(sh.sum[par], warps) * inv_cols);
+    if (tid == 0 && ahead && stages > 1 && next < p.rows) issue();
+    ahead = true;
+    if (warps > 1) dot = join_sum(sums[par] + team * warps, warps);
+    const float mean = -rs * (dot * inv_cols);
     const float2 mean2 = make_float2(mean, mean);  // -mean(gw xh)
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
@@ -537,58 +604,74 @@ __global__ void __launch_bounds__(kRingMaxThreads, 1) k_rmsnorm_bwd_ring(const N
           const float2 t = f2_fma(xh, mean2, gw);
           d[j] = DRES ? f2_fma(t, rs2, d[j]) : f2_mul(t, rs2);
         }
-        vec_store(static_cast<char*>(p.dx) + row * row_bytes + static_cast<int64_t>(v) * 16,
+        vec_store(static_cast<char*>(p.dx) + static_cast<int64_t>(row) * row_bytes + v * 16,
                   vec_narrow<XT>(reinterpret_cast<const float*>(d)));
       }
     }
-    if (stages == 1) {  // rows so wide that one fits: it is refilled once both passes are through
-      __syncthreads();
-      if (tid == 0 && issued < mine) issue();
+    if (stages == 1) {  // one row fits: it is refilled once both passes are through
+      team_any(team, T, false);
+      if (tid == 0 && next < p.rows) issue();
     }
     if (++stage == stages) { stage = 0; phase ^= 1u; }
+    par ^= 1;
+    row = row_next;
   }
-  if (sh.abort_flag) {
-    ring_drain(sh, stages, issued);
-    return;
-  }
-  if (p.part == nullptr) return;
+  if (abort_flag && tid == 0) drain_stages(full[team], stages, stage, phase, next_stage);
+  if (p.part == nullptr && abort_flag == 0) return;
+  __syncthreads();  // every team is through with its ring
+  if (abort_flag) return;
+  float* to = teams == 1 ? p.part + static_cast<int64_t>(blockIdx.x) * p.cols
+                         : reinterpret_cast<float*>(smem) + static_cast<int64_t>(team) * p.cols;
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
     const int v = it * T + tid;
     if (v < nv) {
-      float* to = p.part + static_cast<int64_t>(blockIdx.x) * p.cols + static_cast<int64_t>(v) * VEC;
 #pragma unroll
       for (int j = 0; j < VEC / 2; j += 2) {
         const float2 a = dw[it * (VEC / 2) + j], b = dw[it * (VEC / 2) + j + 1];
-        *reinterpret_cast<float4*>(to + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<float4*>(to + v * VEC + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
       }
     }
+  }
+  if (teams == 1) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.cols; c += blockDim.x) {
+    float t = 0.0f;
+    for (int k = 0; k < teams; ++k) t += reinterpret_cast<const float*>(smem)[k * p.cols + c];
+    p.part[static_cast<int64_t>(blockIdx.x) * p.cols + c] = t;
   }
 }
 
 // dweight[c] = sum of the partials of column c.  A CTA takes 32 columns, its
-// warp w the w-th eighth of the partial rows; the eighths join in order.
-constexpr int kDwWarps = 8;
+// warp w every 32nd partial row from w, all of them in flight at once; the
+// warps' sums join in order.  (8 warps with a run of rows each, eight loads
+// in flight, took 10 us for 296 rows: load latency, five times over.)
+constexpr int kDwWarps = 32;
+constexpr int kDwFlight = 10;   // 10 x 32 rows: the norm's 296 partial rows in one round
 __global__ void __launch_bounds__(32 * kDwWarps) k_column_partials(const float* part, int parts, int cols, void* out, int ot) {
-  __shared__ float s[kDwWarps][32];
+  __shared__ float s[kDwWarps][33];
   pdl_wait();
   pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int c = blockIdx.x * 32 + lane;
-  const int per = (parts + kDwWarps - 1) / kDwWarps;
-  const int b0 = min(parts, warp * per), b1 = min(parts, b0 + per);
   float acc = 0.0f;
   if (c < cols)
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) acc += __ldcg(part + static_cast<int64_t>(b) * cols + c);
+    for (int b0 = warp; b0 < parts; b0 += kDwWarps * kDwFlight) {
+      float f[kDwFlight];
+#pragma unroll
+      for (int k = 0; k < kDwFlight; ++k) {
+        const int b = b0 + k * kDwWarps;
+        f[k] = b < parts ? __ldcg(part + static_cast<int64_t>(b) * cols + c) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kDwFlight; ++k) acc += f[k];
+    }
   s[warp][lane] = acc;
   __syncthreads();
-  if (warp == 0 && c < cols) {
-    float t = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kDwWarps; ++w) t += s[w][lane];
-    elem_store_rt(out, ot, c, t);
-  }
+  // column w of the tile: its 32 warps' sums, joined over the lanes
+  const int cw = blockIdx.x * 32 + warp;
+  const float t = warp_sum(s[lane][warp]);
+  if (lane == 0 && cw < cols) elem_store_rt(out, ot, cw, t);
 }
 
 int sm_count() {
@@ -614,36 +697,56 @@ cudaError_t open_smem(K kernel, std::atomic<uint64_t>& done) {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
-// Launch shape of a ring kernel: E elements per thread, T threads, S stages
-// of stage_bytes.  64 registers a thread let 1024 / T CTAs share an SM, and
-// they share its shared memory.
-struct RingShape {
-  int threads, ctas, stages;
-};
-RingShape ring_shape(int64_t cols, int e, int64_t stage_bytes, int min_stages) {
-  RingShape r;
-  r.threads = static_cast<int>((((cols + e - 1) / e) + 31) / 32 * 32);
-  r.ctas = kRingMaxThreads / r.threads;
-  if (r.ctas > 16) r.ctas = 16;
-  while (r.ctas > 1 && (kRingSmem / r.ctas - 1024) / stage_bytes < min_stages) --r.ctas;
-  const int64_t s = (kRingSmem / r.ctas - 1024) / stage_bytes;
-  r.stages = static_cast<int>(s > kRingStages ? kRingStages : s);
-  return r;
+int ring_threads(int64_t cols, int e) { return static_cast<int>(((cols + e - 1) / e + 31) / 32 * 32); }
+
+// Elements per thread for rows of `cols`: the share that keeps the most of an
+// SM's 512 threads busy, the narrowest of equals (1408 columns of bf16,
+// 47616 rows: 24 elements in 8 CTAs of 64 threads 78 us, 16 elements in 4 of
+// 96 threads 101 us).  32 elements only where 24 do not reach.
+int ring_share(int64_t cols) {
+  if (cols <= 256) return 8;
+  int best = 0;
+  double busy = 0.0;
+  for (int e : {16, 24, 32}) {
+    const int t = ring_threads(cols, e);
+    if (t > ring_max_threads(e, false) || (e == 32 && best != 0)) continue;
+    const double b = static_cast<double>(ring_max_threads(e, false) / t) * static_cast<double>(cols) / e;
+    if (b > busy) { busy = b; best = e; }
+  }
+  return best;
 }
 
-template <int XT, int E, bool RES>
+template <int XT, int E, bool RES, bool WIDE = false>
 cudaError_t norm_ring(const NormArgs& a, const NormParams& p) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = open_smem(k_rmsnorm_ring<XT, E, RES>, done);
+  const cudaError_t e = open_smem(k_rmsnorm_ring<XT, E, RES, WIDE>, done);
   if (e != cudaSuccess) return e;
   const int64_t stage = a.cols * elem_bytes<XT>() * (RES ? 2 : 1);
-  const RingShape r = ring_shape(a.cols, E, stage, 2);
-  const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
+  const int threads = ring_threads(a.cols, E);
+  // as many CTAs on an SM as the registers allow, while two stages each fit
+  int ctas = ring_max_threads(E, WIDE) / threads;
+  if (ctas > 32) ctas = 32;
+  while (ctas > 1 && (kRingSmem / ctas - 1024) / stage < 2) --ctas;
+  int64_t stages = (kRingSmem / ctas - 1024) / stage;
+  if (stages > kRingStages) stages = kRingStages;
+  const int64_t most = static_cast<int64_t>(sm_count()) * ctas;
   const int64_t grid = a.rows < most ? a.rows : most;
   const int64_t per = (a.rows + grid - 1) / grid;
-  const int stages = static_cast<int>(per < r.stages ? per : r.stages);
-  return launch_pdl(k_rmsnorm_ring<XT, E, RES>, dim3(static_cast<unsigned>(grid)), dim3(r.threads),
-                    static_cast<size_t>(stages * stage), a.stream, false, p, stages, device_error_word());
+  if (stages > per) stages = per;
+  return launch_pdl(k_rmsnorm_ring<XT, E, RES, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(threads),
+                    static_cast<size_t>(stages * stage), a.stream, false, p, static_cast<int>(stages), device_error_word());
+}
+
+template <int XT, bool RES>
+cudaError_t norm_ring_any(const NormArgs& a, const NormParams& p) {
+  if (a.cols > kRingMaxCols) return norm_ring<XT, 32, RES, true>(a, p);
+  if (a.rows <= sm_count() && a.cols <= 8 * 1024) return norm_ring<XT, 8, RES>(a, p);
+  switch (ring_share(a.cols)) {
+    case 32: return norm_ring<XT, 32, RES>(a, p);
+    case 24: return norm_ring<XT, 24, RES>(a, p);
+    case 16: return norm_ring<XT, 16, RES>(a, p);
+    default: return norm_ring<XT, 8, RES>(a, p);
+  }
 }
 
 template <int XT>
@@ -654,34 +757,51 @@ cudaError_t norm_run(const NormArgs& a, const NormParams& p) {
                     aligned16(a.y_out) && aligned16(a.weight) && reinterpret_cast<uintptr_t>(a.q) % VEC == 0 &&
                     (p.block == 0 || (group <= 32 && (group & (group - 1)) == 0)) &&
                     a.cols * elem_bytes<XT>() * (a.residual ? 2 : 1) <= kRingSmem - 1024;
-  if (ring) {
-    // 8 elements a thread where a CTA has one row (latency), 16 up to 16384
-    // columns, 32 beyond
-    if (a.rows <= sm_count() && a.cols <= 8 * kRingMaxThreads)
-      return a.residual ? norm_ring<XT, 8, true>(a, p) : norm_ring<XT, 8, false>(a, p);
-    if (a.cols <= 16 * kRingMaxThreads)
-      return a.residual ? norm_ring<XT, 16, true>(a, p) : norm_ring<XT, 16, false>(a, p);
-    return a.residual ? norm_ring<XT, 32, true>(a, p) : norm_ring<XT, 32, false>(a, p);
-  }
+  if (ring) return a.residual ? norm_ring_any<XT, true>(a, p) : norm_ring_any<XT, false>(a, p);
   const int64_t grid = a.rows < 8 * sm_count() ? a.rows : 8 * sm_count();
   return launch_pdl(k_rmsnorm_any<XT>, dim3(static_cast<unsigned>(grid)), dim3(kAnyThreads), 0, a.stream, false, p);
 }
 
 int64_t bwd_parts(int64_t rows) { return rows < kBwdParts ? rows : kBwdParts; }
 
-template <int XT, int E, bool DRES>
+template <int XT, int E, bool DRES, bool WIDE = false>
 cudaError_t bwd_ring(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = open_smem(k_rmsnorm_bwd_ring<XT, E, DRES>, done);
+  const cudaError_t e = open_smem(k_rmsnorm_bwd_ring<XT, E, DRES, WIDE>, done);
   if (e != cudaSuccess) return e;
   const int64_t stage = a.cols * elem_bytes<XT>() * (DRES ? 3 : 2);
-  const RingShape r = ring_shape(a.cols, E, stage, 2);
-  const int64_t most = static_cast<int64_t>(sm_count()) * r.ctas;
+  const int T = ring_threads(a.cols, E);
+  const int half = ring_max_threads(E, WIDE) / 2;
+  // CTAs of half the threads that the registers allow, two to an SM, while
+  // every team has a row
+  int teams = half / T;
+  if (teams > kTeams) teams = kTeams;
+  const int64_t sms = sm_count();
+  while (teams > 1 && (static_cast<int64_t>(teams) * sms >= 2 * a.rows || 2 * teams * stage > kRingSmem / 2 - 2048)) --teams;
+  if (teams < 1) teams = 1;
+  const int ctas = (T * teams <= half && 2 * teams * stage <= kRingSmem / 2 - 2048) ? 2 : 1;
+  int64_t most = sms * ctas;
+  if (most > kBwdParts) most = kBwdParts;
+  grid = (a.rows + teams - 1) / teams;
   if (grid > most) grid = most;
-  const int64_t per = (a.rows + grid - 1) / grid;
-  const int stages = static_cast<int>(per < r.stages ? per : r.stages);
-  return launch_pdl(k_rmsnorm_bwd_ring<XT, E, DRES>, dim3(static_cast<unsigned>(grid)), dim3(r.threads),
-                    static_cast<size_t>(stages * stage), a.stream, false, p, stages, device_error_word());
+  const int64_t per = (a.rows + grid * teams - 1) / (grid * teams);
+  int64_t stages = (kRingSmem / ctas - 2048) / (teams * stage);
+  if (stages > kRingStages) stages = kRingStages;
+  if (stages > per) stages = per;
+  return launch_pdl(k_rmsnorm_bwd_ring<XT, E, DRES, WIDE>, dim3(static_cast<unsigned>(grid)), dim3(T * teams),
+                    static_cast<size_t>(stages * teams * stage), a.stream, false, p, teams, static_cast<int>(stages),
+                    device_error_word());
+}
+
+template <int XT, bool DRES>
+cudaError_t bwd_ring_any(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
+  if (a.cols > kRingMaxCols) return bwd_ring<XT, 32, DRES, true>(a, p, grid);
+  switch (ring_share(a.cols)) {
+    case 32: return bwd_ring<XT, 32, DRES>(a, p, grid);
+    case 24: return bwd_ring<XT, 24, DRES>(a, p, grid);
+    case 16: return bwd_ring<XT, 16, DRES>(a, p, grid);
+    default: return bwd_ring<XT, 8, DRES>(a, p, grid);
+  }
 }
 
 // grid: the largest number of CTAs (and partial rows); the number launched.
@@ -690,12 +810,8 @@ cudaError_t bwd_run(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid)
   constexpr int VEC = vec_elems<XT>();
   const int64_t stage = a.cols * elem_bytes<XT>() * (a.dres ? 3 : 2);
   const bool ring = a.cols % VEC == 0 && aligned16(a.dy) && aligned16(a.h) && aligned16(a.dres) && aligned16(a.dx) &&
-                    aligned16(a.weight) && stage <= kRingSmem - 1024;
-  if (ring) {
-    if (a.cols <= 16 * kRingMaxThreads)
-      return a.dres ? bwd_ring<XT, 16, true>(a, p, grid) : bwd_ring<XT, 16, false>(a, p, grid);
-    return a.dres ? bwd_ring<XT, 32, true>(a, p, grid) : bwd_ring<XT, 32, false>(a, p, grid);
-  }
+                    aligned16(a.weight) && stage <= kRingSmem - 2048;
+  if (ring) return a.dres ? bwd_ring_any<XT, true>(a, p, grid) : bwd_ring_any<XT, false>(a, p, grid);
   const size_t smem = p.part ? static_cast<size_t>(a.cols) * 4 : 0;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(k_rmsnorm_bwd_any<XT>, cudaFuncAttributeMaxDynamicSharedMemorySize,

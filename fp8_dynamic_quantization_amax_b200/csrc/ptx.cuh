@@ -73,6 +73,14 @@ __device__ __noinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile 
   }
 }
 
+// The same with the first look inline: a barrier that is already there costs
+// no call.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                                 unsigned* err_word, unsigned timeout_bit) {
+  if (mbar_try_wait(smem_u32(bar), parity)) return true;
+  return mbar_wait(bar, parity, abort_flag, err_word, timeout_bit);
+}
+
 // 1-D bulk copy global -> shared (TMA), completing `bytes` on the mbarrier.
 // Both addresses 16-byte aligned, bytes a multiple of 16.
 __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
