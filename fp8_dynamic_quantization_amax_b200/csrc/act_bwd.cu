@@ -4,7 +4,7 @@
 //
 // One pass over the data.  A CTA takes a strip of 256 columns (a warp's 32
 // lanes x 8 columns) and a band of rows; warp w of the CTA takes rows w,
-// w + 8, ... of the band.  With dbias each lane adds its columns' f32 dz in
+// w + 8, ... of the band, four rows' loads in flight.  With dbias each lane adds its columns' f32 dz in
 // row order, the eight warps join in order, and the band's sums go to the
 // workspace; a second launch adds the bands in order.  The order of the sums
 // is fixed, and the workspace needs no initial state.
@@ -21,8 +21,9 @@ namespace {
 constexpr int kAbWarps = 8;
 constexpr int kAbVec = 8;                    // columns per lane
 constexpr int kAbStrip = 32 * kAbVec;        // columns per strip
-constexpr int64_t kAbMinBand = 64;           // rows per band, at least
-constexpr int64_t kAbCtas = 8 * 148;         // aim: this many CTAs
+constexpr int kAbRows = 4;                   // a warp's rows in flight
+constexpr int64_t kAbMinBand = kAbWarps * kAbRows;  // rows per band, at least
+constexpr int64_t kAbCtas = 16 * 148;        // aim: this many CTAs
 
 __host__ __device__ inline int64_t ab_strips(int64_t cols) { return (cols + kAbStrip - 1) / kAbStrip; }
 inline int64_t ab_band_rows(int64_t rows, int64_t cols) {
@@ -58,7 +59,8 @@ __device__ __forceinline__ float2 decode2(uint32_t c2) {
 }
 
 template <int GT, int FMT, int ACT>
-__global__ void __launch_bounds__(32 * kAbWarps) k_act_bwd(const AbParams p) {
+__global__ void __launch_bounds__(32 * kAbWarps, 4) k_act_bwd(const AbParams p) {
+  constexpr int GV = GT == 0 ? 2 : 1;  // 16-byte vectors of g per lane and row
   __shared__ float red[kAbWarps][kAbStrip];
   pdl_wait();
   pdl_launch_dependents();
@@ -68,37 +70,51 @@ __global__ void __launch_bounds__(32 * kAbWarps) k_act_bwd(const AbParams p) {
   const int c0 = strip * kAbStrip + lane * kAbVec;
   const int64_t r0 = band * p.band_rows;
   const int64_t r1 = min(p.rows, r0 + p.band_rows);
-  float acc[kAbVec];
+  float2 acc[kAbVec / 2];
 #pragma unroll
-  for (int j = 0; j < kAbVec; ++j) acc[j] = 0.0f;
+  for (int j = 0; j < kAbVec / 2; ++j) acc[j] = make_float2(0.0f, 0.0f);
   if (c0 < p.cols) {  // cols % 16 == 0: a lane's 8 columns are all inside
-    const int b = c0 / p.block;
-    for (int64_t r = r0 + warp; r < r1; r += kAbWarps) {
-      const int64_t i = r * p.cols + c0;
-      const uint2 zc = __ldg(reinterpret_cast<const uint2*>(p.zq + i));
-      const float sc = __ldg(p.zs + r * p.nb + b);
-      float g[kAbVec];
-      const char* gp = static_cast<const char*>(p.g) + i * elem_bytes<GT>();
-      vec_widen<GT>(vec_load(gp), g);
-      if (GT == 0) vec_widen<GT>(vec_load(gp + 16), g + 4);
-      float d[kAbVec];
+    const float* zs = p.zs + c0 / p.block;
+    for (int64_t r = r0 + warp; r < r1; r += kAbWarps * kAbRows) {
+      uint4 gr[kAbRows][GV];
+      uint2 zc[kAbRows];
+      float sc[kAbRows];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 z = decode2<FMT>((j < 2 ? zc.x : zc.y) >> (16 * (j & 1)));
-        d[2 * j] = g[2 * j] * act_backward<ACT>(__fmul_rn(z.x, sc));
-        d[2 * j + 1] = g[2 * j + 1] * act_backward<ACT>(__fmul_rn(z.y, sc));
+      for (int k = 0; k < kAbRows; ++k) {
+        const int64_t row = r + k * kAbWarps;
+        if (row < r1) {
+          const int64_t i = row * p.cols + c0;
+          const char* gp = static_cast<const char*>(p.g) + i * elem_bytes<GT>();
+#pragma unroll
+          for (int v = 0; v < GV; ++v) gr[k][v] = vec_load(gp + 16 * v);
+          zc[k] = __ldg(reinterpret_cast<const uint2*>(p.zq + i));
+          sc[k] = __ldg(zs + row * p.nb);
+        }
       }
-      char* dp = static_cast<char*>(p.dz) + i * elem_bytes<GT>();
-      vec_store(dp, vec_narrow<GT>(d));
-      if (GT == 0) vec_store(dp + 16, vec_narrow<GT>(d + 4));
 #pragma unroll
-      for (int j = 0; j < kAbVec; ++j) acc[j] += d[j];
+      for (int k = 0; k < kAbRows; ++k) {
+        const int64_t row = r + k * kAbWarps;
+        if (row < r1) {
+          float2 g[kAbVec / 2], d[kAbVec / 2];
+#pragma unroll
+          for (int v = 0; v < GV; ++v) vec_widen<GT>(gr[k][v], reinterpret_cast<float*>(g) + 4 * v);
+#pragma unroll
+          for (int j = 0; j < kAbVec / 2; ++j) {
+            const float2 z = f2_mul(decode2<FMT>((j < 2 ? zc[k].x : zc[k].y) >> (16 * (j & 1))), act_both(sc[k]));
+            d[j] = f2_mul(g[j], act_backward<ACT>(z));
+            acc[j] = f2_add(acc[j], d[j]);
+          }
+          char* dp = static_cast<char*>(p.dz) + (row * p.cols + c0) * elem_bytes<GT>();
+#pragma unroll
+          for (int v = 0; v < GV; ++v) vec_store(dp + 16 * v, vec_narrow<GT>(reinterpret_cast<const float*>(d) + 4 * v));
+        }
+      }
     }
   }
   if (p.part == nullptr) return;
 #pragma unroll
-  for (int j = 0; j < kAbVec; j += 4)
-    *reinterpret_cast<float4*>(&red[warp][lane * kAbVec + j]) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+  for (int j = 0; j < kAbVec / 2; j += 2)
+    *reinterpret_cast<float4*>(&red[warp][lane * kAbVec + 2 * j]) = make_float4(acc[j].x, acc[j].y, acc[j + 1].x, acc[j + 1].y);
   __syncthreads();
   const int c = strip * kAbStrip + static_cast<int>(threadIdx.x);
   if (c < p.cols) {

@@ -406,7 +406,11 @@ __device__ __forceinline__ float chunk_f32_to_fp8(const float (&z)[32], int fmt,
 template <int ACT>
 __device__ __forceinline__ void chunk_act(float (&z)[32]) {
 #pragma unroll
-  for (int j = 0; j < 32; ++j) z[j] = act_forward<ACT>(z[j]);
+  for (int j = 0; j < 16; ++j) {
+    const float2 r = act_forward<ACT>(make_float2(z[2 * j], z[2 * j + 1]));
+    z[2 * j] = r.x;
+    z[2 * j + 1] = r.y;
+  }
 }
 
 // One epilogue warp's share of a tile with the activation epilogue: as

@@ -61,6 +61,11 @@ def check(out, z, err, act, res):
     assert bool((off <= tol).all()), "%d off, worst %g of its bound" % (int((off > tol).sum()), float((off / tol).max()))
 
 
+# up to 16 rows: one group of columns, more than the SMs, several batches, K of one step, an odd number and many
+SHAPES += [(1, 8, 64), (2, 16, 16), (4, 1184, 1040), (7, 10056, 208), (8, 20000, 1024), (9, 40, 8192), (12, 3000, 2064),
+           (15, 28680, 128), (16, 8192, 28672)]
+
+
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
 def test_bias_activation_residual(shape):
     M, N, K = shape
@@ -97,8 +102,9 @@ def test_checkpoint(shape, act):
 
 
 def test_no_activation_is_the_plain_gemm():
-    # without activation and residual: bit for bit the existing epilogue, bias or not
-    for M, N, K in ((16, 8192, 512), (300, 272, 144), (700, 2048, 128), (8200, 2048, 32)):
+    # without activation and residual: bit for bit the existing epilogue, bias or not, on the same tiles (up to 16 rows
+    # another kernel sums in another order)
+    for M, N, K in ((17, 8192, 512), (300, 272, 144), (700, 2048, 128), (8200, 2048, 32)):
         xq, wq, xs, ws, bias, _ = operands(M, N, K, seed=K)
         assert torch.equal(H.hq_gemm_a8w8_act(xq, wq, xs, ws), H.hq_gemm_a8w8(xq, wq, xs, ws))
         assert torch.equal(H.hq_gemm_a8w8_act(xq, wq, xs, ws, bias=bias), H.hq_gemm_a8w8_ex(xq, wq, xs, ws, bias=bias))
