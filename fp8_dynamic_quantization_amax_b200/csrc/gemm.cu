@@ -44,9 +44,26 @@ namespace {
 
 constexpr int kBM = 128;            // tile rows (MMA M)
 constexpr int kBKBytes = 128;       // K bytes per stage = one 128B swizzle row
-constexpr int kGemmThreads = 320;   // CTA-pair kernel: TMA, MMA, 8 epilogue warps
-constexpr int kGemm1Threads = 320;  // 1-CTA kernel: TMA, MMA, 8 epilogue warps
 constexpr int kMaxExperts = 1024;
+// The activation epilogue has 16 warps, four to a scheduler: a chunk of 32
+// columns is some 700 dependent-latency-bound instructions with GELU, and
+// where a CTA has one tile (or one accumulator) all of that is exposed.
+constexpr int kActWarps = 16;
+template <bool ACT>
+constexpr int epi_warps() {
+  return ACT ? kActWarps : 8;
+}
+template <bool ACT>
+constexpr int gemm_threads() {
+  return 64 + 32 * epi_warps<ACT>();
+}
+// dynamic shared memory behind the stages: per epilogue warp a 2 KB staging
+// tile and its column scales, or (ACT: it stores straight from registers)
+// its columns' scales and biases
+template <bool ACT>
+constexpr int epi_smem(int chunks) {
+  return ACT ? kActWarps * ((chunks + 3) / 4) * 32 * 8 : 8 * 2048 + 8 * ((chunks + 1) / 2) * 32 * 4;
+}
 constexpr unsigned long long kDrainLimitNs = ptx::kDrainLimitNs;
 
 struct Params {
@@ -83,6 +100,7 @@ struct Params {
   uint8_t* zq;           // codes [M, N] or null
   float* zs;             // dequant scales [M, N / 32]
   int zfmt;
+  int wide;              // out, res and zq rows start on 32-byte boundaries
 };
 
 // ------------------------------------------------------------ PTX wrappers
@@ -413,46 +431,103 @@ __device__ __forceinline__ void chunk_act(float (&z)[32]) {
   }
 }
 
-// One epilogue warp's share of a tile with the activation epilogue: as
-// epilogue_chunks, but z = acc * scales (+ bias) stays in f32 through the
-// checkpoint's quantize, the activation and the residual addition, and is
-// rounded to bf16 once.
+// Whole sectors of the residual, the result and the checkpoint, each touched
+// once: evicted first, so that they do not push the operands out of L2 (with
+// plain stores the 4096 x 28672 x 8192 product took 781 us against 701).
+__device__ __forceinline__ void ld_global_v8(const void* p, uint32_t (&r)[8]) {
+  asm volatile("ld.global.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
+               : "memory");
+}
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
+// The activation epilogue's column scales and biases of one warp's chunks of
+// a tile (chunk group + 4 j of 32 columns; lane: column), asked for before
+// the accumulator is waited for and put into the warp's shared memory after:
+// [j][32 scales | 32 biases].
+template <int kMyChunks>
+struct ActColumns {
+  float s[kMyChunks], b[kMyChunks];
+  __device__ __forceinline__ void load(const Params& p, int col0, int group, int lane) {
+#pragma unroll
+    for (int j = 0; j < kMyChunks; ++j) {
+      const int n = col0 + (group + 4 * j) * 32 + lane;
+      s[j] = n < p.N ? __ldg(p.ws + (p.ws_bcast ? 0 : n)) : 0.0f;
+      b[j] = (n < p.N && p.bias != nullptr) ? __uint_as_float(static_cast<uint32_t>(__ldg(p.bias + n)) << 16) : 0.0f;
+    }
+  }
+  __device__ __forceinline__ void put(float* sm, int lane) const {
+#pragma unroll
+    for (int j = 0; j < kMyChunks; ++j) {
+      sm[j * 64 + lane] = s[j];
+      sm[j * 64 + 32 + lane] = b[j];
+    }
+  }
+};
+
+// 32 residual columns from n0 of a lane's row (as many as lie before col_end)
+__device__ __forceinline__ void load_residual(const uint16_t* row, int n0, int col_end, bool wide, uint32_t (&r)[16]) {
+  if (wide && n0 + 32 <= col_end) {
+    ld_global_v8(row + n0, *reinterpret_cast<uint32_t(*)[8]>(r));
+    ld_global_v8(row + n0 + 16, *reinterpret_cast<uint32_t(*)[8]>(r + 8));
+  } else {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      if (n0 + 8 * k < col_end) u = ld_global_v4(row + n0 + 8 * k);
+      r[4 * k] = u.x; r[4 * k + 1] = u.y; r[4 * k + 2] = u.z; r[4 * k + 3] = u.w;
+    }
+  }
+}
+
+// One epilogue warp's share of a tile with the activation epilogue: chunks
+// group, group + 4, ... of 32 columns.  z = acc * scales (+ bias) stays in
+// f32 through the checkpoint's quantize, the activation and the residual
+// addition, and is rounded to bf16 once.  A lane holds a row: it stores its
+// 64 bytes of out and 32 of codes as whole 32-byte sectors (p.wide) or in
+// 16-byte pieces.  res holds the first chunk's residual on entry; the next
+// chunk's is asked for as soon as one is used.
 template <int kChunks>
-__device__ __forceinline__ void epilogue_chunks_act(uint32_t tacc, int half, int lane, int col0, int col_end,
-                                                    int tile_end, int row0, int row, bool vrow, bool tma_ok,
-                                                    bool has_acc, float xsv, const float* wsh, const Params& p,
-                                                    uint8_t* sb, const CUtensorMap* tm_out, uint64_t out_pol) {
+__device__ __forceinline__ void epilogue_chunks_act(uint32_t tacc, int group, int col0, int col_end, int row, bool vrow,
+                                                    bool has_acc, float xsv, const float* cols, const Params& p,
+                                                    uint32_t (&res)[16]) {
   const int64_t rbase = static_cast<int64_t>(vrow ? row : 0) * p.N;
   uint16_t* orow = p.out + rbase;
+  const bool with_res = p.res != nullptr && vrow;
+  const float2 xs2 = make_float2(xsv, xsv);
 #pragma unroll 1
-  for (int j = 0; half + 2 * j < kChunks; ++j) {
-    const int n0 = col0 + (half + 2 * j) * 32;
+  for (int j = 0; group + 4 * j < kChunks; ++j) {
+    const int n0 = col0 + (group + 4 * j) * 32;
     uint32_t v[32];
-    tmem_ld32(tacc + static_cast<uint32_t>((half + 2 * j) * 32), v);
-    if (n0 >= col_end) continue;
-    const float* sc = wsh + j * 32;
+    tmem_ld32(tacc + static_cast<uint32_t>((group + 4 * j) * 32), v);
+    if (n0 >= col_end) return;
     float z[32];
-    if (p.bias == nullptr) {
+    const float4* sc = reinterpret_cast<const float4*>(cols + j * 64);
+    const float4* bi = reinterpret_cast<const float4*>(cols + j * 64 + 32);
 #pragma unroll
-      for (int k = 0; k < 16; ++k)
-        scale2(has_acc ? __uint_as_float(v[2 * k]) : 0.0f, has_acc ? __uint_as_float(v[2 * k + 1]) : 0.0f, sc[2 * k],
-               sc[2 * k + 1], xsv, z[2 * k], z[2 * k + 1]);
-    } else {
-      const uint32_t* bp = reinterpret_cast<const uint32_t*>(p.bias) + (n0 >> 1);
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint32_t bb = (n0 + 2 * k < p.N) ? __ldg(bp + k) : 0u;
-        scale2_bias(has_acc ? __uint_as_float(v[2 * k]) : 0.0f, has_acc ? __uint_as_float(v[2 * k + 1]) : 0.0f,
-                    sc[2 * k], sc[2 * k + 1], xsv, __uint_as_float(bb << 16), __uint_as_float(bb & 0xFFFF0000u),
-                    z[2 * k], z[2 * k + 1]);
-      }
+    for (int k = 0; k < 8; ++k) {
+      const float4 s4 = sc[k], b4 = bi[k];
+      const float2 a0 = has_acc ? make_float2(__uint_as_float(v[4 * k]), __uint_as_float(v[4 * k + 1])) : make_float2(0.0f, 0.0f);
+      const float2 a1 = has_acc ? make_float2(__uint_as_float(v[4 * k + 2]), __uint_as_float(v[4 * k + 3])) : make_float2(0.0f, 0.0f);
+      const float2 z0 = f2_fma(a0, f2_mul(make_float2(s4.x, s4.y), xs2), make_float2(b4.x, b4.y));
+      const float2 z1 = f2_fma(a1, f2_mul(make_float2(s4.z, s4.w), xs2), make_float2(b4.z, b4.w));
+      z[4 * k] = z0.x; z[4 * k + 1] = z0.y; z[4 * k + 2] = z1.x; z[4 * k + 3] = z1.y;
     }
     if (p.zq != nullptr) {  // N % 32 == 0: the chunk is one whole block of the row
       uint32_t c4[8];
       const float m = chunk_f32_to_fp8(z, p.zfmt, c4);
       if (vrow) {
-        st_global_v4(p.zq + rbase + n0, c4[0], c4[1], c4[2], c4[3]);
-        st_global_v4(p.zq + rbase + n0 + 16, c4[4], c4[5], c4[6], c4[7]);
+        if (p.wide) {
+          st_global_v8(p.zq + rbase + n0, c4);
+        } else {
+          st_global_v4(p.zq + rbase + n0, c4[0], c4[1], c4[2], c4[3]);
+          st_global_v4(p.zq + rbase + n0 + 16, c4[4], c4[5], c4[6], c4[7]);
+        }
         p.zs[static_cast<int64_t>(row) * (p.N >> 5) + (n0 >> 5)] = __fdiv_rn(1.0f, m);
       }
     }
@@ -463,39 +538,26 @@ __device__ __forceinline__ void epilogue_chunks_act(uint32_t tacc, int half, int
       case kActSilu: chunk_act<kActSilu>(z); break;
       default: break;
     }
-    if (p.res != nullptr && vrow) {
+    if (with_res) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (n0 + 8 * k >= col_end) break;
-        const uint4 u = ld_global_v4(p.res + rbase + n0 + 8 * k);
-        const uint32_t w4[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          z[8 * k + 2 * i] += __uint_as_float(w4[i] << 16);
-          z[8 * k + 2 * i + 1] += __uint_as_float(w4[i] & 0xFFFF0000u);
-        }
+      for (int k = 0; k < 16; ++k) {
+        z[2 * k] += __uint_as_float(res[k] << 16);
+        z[2 * k + 1] += __uint_as_float(res[k] & 0xFFFF0000u);
       }
+      if (group + 4 * (j + 1) < kChunks) load_residual(p.res + rbase, n0 + 128, col_end, p.wide, res);
     }
     uint32_t w[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) w[k] = pack_bf16x2(z[2 * k], z[2 * k + 1]);
-    if (tma_ok && n0 + 32 <= tile_end) {  // staging tile and TMA store, as epilogue_chunks
-      if (lane == 0) bulk_wait_read_le0();
-      __syncwarp();
+    if (vrow) {
+      if (p.wide && n0 + 32 <= col_end) {
+        st_global_v8(orow + n0, w);
+        st_global_v8(orow + n0 + 16, w + 8);
+      } else {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        st_shared_v4(sb + lane * 64 + ((k ^ ((lane >> 1) & 3)) << 4), w[4 * k], w[4 * k + 1], w[4 * k + 2],
-                     w[4 * k + 3]);
-      ptx::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        tma_store_2d(tm_out, sb, n0, row0, out_pol);
-        bulk_commit_group();
+        for (int k = 0; k < 4; ++k)
+          if (n0 + 8 * k < col_end) st_global_v4(orow + n0 + 8 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
       }
-    } else if (vrow) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (n0 + 8 * k < col_end) st_global_v4(orow + n0 + 8 * k, w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
     }
   }
 }
@@ -585,7 +647,7 @@ __device__ void build_tile_prefix(const Params& p, int* prefix, int* starts) {
 // one 128-byte piece per row, so more of each opened DRAM page is used.
 // ACT: the activation epilogue (dense a8w8 only) instead of the plain one.
 template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1, bool ACT = false>
-__global__ void __launch_bounds__(kGemm1Threads, 1)
+__global__ void __launch_bounds__(gemm_threads<ACT>(), 1)
     k_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
            const __grid_constant__ CUtensorMap tm_out, const Params p) {
   static_assert((STAGES * KPS - 1) * AROWS * kBKBytes + kBM * kBKBytes <= STAGES * KPS * (AROWS + BN) * kBKBytes,
@@ -610,8 +672,8 @@ __global__ void __launch_bounds__(kGemm1Threads, 1)
   __shared__ __align__(8) uint64_t final_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ int tile_prefix[kMaxExperts + 1];
-  __shared__ int row_start[kMaxExperts + 1];
+  __shared__ int tile_prefix[ACT ? 1 : kMaxExperts + 1];  // grouped only
+  __shared__ int row_start[ACT ? 1 : kMaxExperts + 1];
 
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);  // 1024-byte aligned stages
@@ -632,7 +694,7 @@ __global__ void __launch_bounds__(kGemm1Threads, 1)
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull_bar[a], 1);
-      mbar_init(&tempty_bar[a], 8);  // one arrive per epilogue warp
+      mbar_init(&tempty_bar[a], epi_warps<ACT>());  // one arrive per epilogue warp
     }
     mbar_init(&final_bar, 1);
     abort_flag = 0;
@@ -761,6 +823,39 @@ __global__ void __launch_bounds__(kGemm1Threads, 1)
     const float qm = (p.qout != nullptr && p.qbs == nullptr) ? __ldcg(p.ring + p.ring_len) : 0.0f;  // the delayed multiplier
     const bool has_acc = p.nkb > 0;
     const uint16_t* bias = (KIND == 0) ? p.bias : nullptr;
+    if constexpr (ACT) {
+      constexpr int kActChunks = (kChunks + 3) / 4;
+      const int group = ew >> 2;
+      float* cols = reinterpret_cast<float*>(sOut) + ew * kActChunks * 64;
+      int i = 0;
+      for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
+        const int acc = i & 1;
+        // what does not depend on the accumulator is asked for before the wait
+        const Tile T = decode_tile<kBM, BN>(t, p, tile_prefix, row_start);
+        const int row = T.row_lo + quad * 32 + lane;
+        const bool vrow = row < T.row_hi;
+        const int ncap = min(p.N, T.col0 + BN);
+        const float xsv = vrow ? __ldg(p.xs + (p.xs_bcast ? 0 : row)) : 0.0f;
+        ActColumns<kActChunks> ac;
+        ac.load(p, T.col0, group, lane);
+        uint32_t res[16];
+        if (p.res != nullptr && vrow)
+          load_residual(p.res + static_cast<int64_t>(row) * p.N, T.col0 + group * 32, ncap, p.wide, res);
+        // the warp agrees on giving up: the TMEM loads below are warp-wide
+        if (__any_sync(0xFFFFFFFFu, !mbar_wait(&tfull_bar[acc], (i >> 1) & 1, &abort_flag))) break;
+        tc_fence_after();
+        ac.put(cols, lane);
+        __syncwarp();
+        // a warp whose rows all lie past the tile's has nothing to store
+        if (T.row_lo + quad * 32 < T.row_hi)
+          epilogue_chunks_act<kChunks>(
+              tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride, group,
+              T.col0, ncap, row, vrow, has_acc, xsv, cols, p, res);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty_bar[acc]);
+      }
+    } else {
     int i = 0;
     for (int t = blockIdx.x; t < total; t += gridDim.x, ++i) {
       const int acc = i & 1;
@@ -799,24 +894,21 @@ __global__ void __launch_bounds__(kGemm1Threads, 1)
       float* qsrow = (KIND == 0 && p.qbs != nullptr) ? p.qbs + static_cast<int64_t>(vrow ? row : 0) * (p.N >> 5) : nullptr;
       const uint32_t tacc =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride;
-      if constexpr (ACT)
-        epilogue_chunks_act<kChunks>(tacc, half, lane, T.col0, ncap, T.col0 + BN, row0, row, vrow, tma_ok, has_acc, xsv,
-                                     wsh, p, sb, &tm_out, out_pol);
-      else
-        epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, ncap, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
-                                       wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
+      epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, ncap, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
+                                     wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&tempty_bar[acc]);
     }
-    if (lane == 0) bulk_wait_all();  // stores complete before the CTA's shared memory goes
+    }
+    if (!ACT && lane == 0) bulk_wait_all();  // stores complete before the CTA's shared memory goes
     __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   if (KIND == 0 && p.qout != nullptr && p.qbs == nullptr)
-    finalize_fp8_out<kGemm1Threads / 32>(p, fmaxf(qam, __uint_as_float(qraw << 16)));
+    finalize_fp8_out<gemm_threads<ACT>() / 32>(p, fmaxf(qam, __uint_as_float(qraw << 16)));
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(kTmemCols)
@@ -898,12 +990,14 @@ void set_fused_epilogue(const GemmArgs& a, Params& p) {
   p.zq = a.z_q;
   p.zs = a.z_scales;
   p.zfmt = a.z_fmt;
+  const auto at32 = [](const void* q) { return (reinterpret_cast<uintptr_t>(q) & 31u) == 0; };
+  p.wide = at32(a.out) && at32(a.residual) && a.N % 16 == 0 && (a.z_q == nullptr || at32(a.z_q));
 }
 
 template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1, bool ACT = false>
 cudaError_t run(const GemmArgs& a, std::string* msg) {
   constexpr int kElem = (KIND == 0) ? 1 : 2;
-  constexpr int kSmem = STAGES * KPS * (AROWS + BN) * kBKBytes + 8 * 2048 + 8 * (((BN + 31) / 32 + 1) / 2) * 32 * 4 + 1024;
+  constexpr int kSmem = STAGES * KPS * (AROWS + BN) * kBKBytes + epi_smem<ACT>((BN + 31) / 32) + 1024;
   static_assert(kSmem + 8352 <= 232448, "shared memory over the 227 KB per-CTA limit");
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -962,7 +1056,7 @@ cudaError_t run(const GemmArgs& a, std::string* msg) {
     tiles_bound = (static_cast<int64_t>(p.m_tiles) + a.E) * p.n_tiles;
   int grid = static_cast<int>(tiles_bound < sms ? tiles_bound : sms);
   if (grid < 1) grid = 1;
-  return launch_pdl(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, dim3(grid), dim3(kGemm1Threads), kSmem, a.stream, false,
+  return launch_pdl(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, dim3(grid), dim3(gemm_threads<ACT>()), kSmem, a.stream, false,
                     ta, tb, to, p);
 }
 
@@ -1031,7 +1125,7 @@ __device__ __forceinline__ void mma_issue_pair(uint32_t d_tmem, uint64_t adesc, 
 // MMAs against the same A stage (fewer operand bytes per flop) into one
 // accumulator of up to 512 columns; the epilogue then does not overlap.
 template <int KIND, int SUBN, int NSUB, int STAGES, bool ACT = false>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<ACT>(), 1)
     k_gemm2(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
             const __grid_constant__ CUtensorMap tm_out, const Params p) {
   constexpr int BN = SUBN * NSUB;
@@ -1058,8 +1152,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   __shared__ __align__(8) uint64_t final_bar;
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ int tile_prefix[kMaxExperts + 1];
-  __shared__ int row_start[kMaxExperts + 1];
+  __shared__ int tile_prefix[ACT ? 1 : kMaxExperts + 1];  // grouped only
+  __shared__ int row_start[ACT ? 1 : kMaxExperts + 1];
 
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* smem = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
@@ -1081,7 +1175,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     for (int a = 0; a < kAccs; ++a) {
       mbar_init(&tfull_bar[a], 1);
-      mbar_init(&tempty_bar[a], 16);  // leader: 8 epilogue warps x 2 CTAs
+      mbar_init(&tempty_bar[a], 2 * epi_warps<ACT>());  // leader: the epilogue warps of both CTAs
     }
     mbar_init(&final_bar, 1);
     abort_flag = 0;
@@ -1221,6 +1315,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     uint32_t tempty_leader[kAccs];
 #pragma unroll
     for (int a = 0; a < kAccs; ++a) tempty_leader[a] = mapa_shared(smem_u32(&tempty_bar[a]), 0);
+    if constexpr (ACT) {
+      constexpr int kActChunks = (kChunks + 3) / 4;
+      const int group = ew >> 2;
+      float* cols = reinterpret_cast<float*>(sOut) + ew * kActChunks * 64;
+      int i = 0;
+      for (int t = cluster; t < total; t += nclusters, ++i) {
+        const int acc = i % kAccs;
+        const Tile T = decode_tile<256, BN>(t, p, tile_prefix, row_start);
+        const int row0 = T.row_lo + static_cast<int>(rank) * 128 + quad * 32;  // this warp's first row
+        const int row = row0 + lane;
+        const bool vrow = row < T.row_hi;
+        const float xsv = vrow ? __ldg(p.xs + (p.xs_bcast ? 0 : row)) : 0.0f;
+        ActColumns<kActChunks> ac;
+        ac.load(p, T.col0, group, lane);
+        uint32_t res[16];
+        if (p.res != nullptr && vrow)
+          load_residual(p.res + static_cast<int64_t>(row) * p.N, T.col0 + group * 32, p.N, p.wide, res);
+        if (__any_sync(0xFFFFFFFFu, !mbar_wait(&tfull_bar[acc], (i / kAccs) & 1, &abort_flag))) break;
+        tc_fence_after();
+        ac.put(cols, lane);
+        __syncwarp();
+        if (row0 < T.row_hi)
+          epilogue_chunks_act<kChunks>(
+              tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride, group,
+              T.col0, p.N, row, vrow, has_acc, xsv, cols, p, res);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
+      }
+    } else {
     int i = 0;
     for (int t = cluster; t < total; t += nclusters, ++i) {
       const int acc = i % kAccs;
@@ -1259,24 +1383,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       float* qsrow = (KIND == 0 && p.qbs != nullptr) ? p.qbs + static_cast<int64_t>(vrow ? row : 0) * (p.N >> 5) : nullptr;
       const uint32_t tacc =
           tmem_base + (static_cast<uint32_t>(quad * 32) << 16) + static_cast<uint32_t>(acc) * kAccStride;
-      if constexpr (ACT)
-        epilogue_chunks_act<kChunks>(tacc, half, lane, T.col0, p.N, T.col0 + BN, row0, row, vrow, tma_ok, has_acc, xsv,
-                                     wsh, p, sb, &tm_out, out_pol);
-      else
-        epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, p.N, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
-                                       wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
+      epilogue_chunks<KIND, kChunks>(tacc, half, lane, T.col0, p.N, T.col0 + BN, row0, vrow, tma_ok, has_acc, xsv,
+                                     wsh, p, bias, orow, qrow, qsrow, qm, qraw, qam, sb, &tm_out, out_pol);
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive_cluster(tempty_leader[acc]);
     }
-    if (lane == 0) bulk_wait_all();  // stores complete before the CTA's shared memory goes
+    }
+    if (!ACT && lane == 0) bulk_wait_all();  // stores complete before the CTA's shared memory goes
     __syncwarp();
   }
 
   tc_fence_before();
   __syncthreads();
   if (KIND == 0 && p.qout != nullptr && p.qbs == nullptr)
-    finalize_fp8_out<kGemmThreads / 32>(p, fmaxf(qam, __uint_as_float(qraw << 16)));
+    finalize_fp8_out<gemm_threads<ACT>() / 32>(p, fmaxf(qam, __uint_as_float(qraw << 16)));
   cluster_sync();  // no CTA leaves while its peer may still touch its shared memory
   if (warp == 1) {
     tc_fence_after();
@@ -1290,7 +1411,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   constexpr int BN = SUBN * NSUB;
   constexpr int kElem = (KIND == 0) ? 1 : 2;
   constexpr int kSmem =
-      STAGES * (128 + BN / 2) * kBKBytes + 8 * 2048 + 8 * ((BN / 32 + 1) / 2) * 32 * 4 + 1024;
+      STAGES * (128 + BN / 2) * kBKBytes + epi_smem<ACT>(BN / 32) + 1024;
   static_assert(kSmem + 8400 <= 232448, "shared memory over the 227 KB per-CTA limit");
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -1301,7 +1422,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(148, 1, 1);
-    cfg.blockDim = dim3(kGemmThreads, 1, 1);
+    cfg.blockDim = dim3(gemm_threads<ACT>(), 1, 1);
     cfg.dynamicSmemBytes = kSmem;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeClusterDimension;
@@ -1363,7 +1484,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   const int64_t tiles = static_cast<int64_t>(p.m_tiles + (a.offsets != nullptr ? a.E : 0)) * p.n_tiles;
   if (tiles < clusters) clusters = static_cast<int>(tiles);
   if (clusters < 1) clusters = 1;
-  return launch_pdl(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, dim3(2 * clusters), dim3(kGemmThreads), kSmem, a.stream,
+  return launch_pdl(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, dim3(2 * clusters), dim3(gemm_threads<ACT>()), kSmem, a.stream,
                     false, ta, tb, to, p);
 }
 
