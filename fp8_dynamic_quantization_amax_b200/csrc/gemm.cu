@@ -112,6 +112,8 @@ using ptx::mbar_arrive;
 // Bounded wait; a timeout is recorded in the device error word.
 __device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           unsigned long long limit = ptx::kWaitLimitNs) {
+  // the first look inline: a call per stage cost the MMA issuer 100 cycles
+  if (ptx::mbar_try_wait(smem_u32(bar), parity)) return true;
   return ptx::mbar_wait(bar, parity, abort_flag, &g_device_error, kDevErrTimeout, limit);
 }
 
@@ -765,23 +767,23 @@ __global__ void __launch_bounds__(gemm_threads<ACT>(), 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------- MMA issuer
-    int stage = 0;
-    uint32_t phase = 0;
-    bool issued = false;
-    bool stop = false;
-    int i = 0;
-    for (int t = blockIdx.x; t < total && !stop; t += gridDim.x, ++i) {
-      const int acc = i & 1;
-      const uint32_t acc_phase = (i >> 1) & 1;
-      // the warp agrees on giving up a wait, so that no lane is left at a
-      // warp-wide step after another has left
-      if (__any_sync(0xFFFFFFFFu, !mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, &abort_flag))) break;
-      tc_fence_after();
-      const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAccStride;
-      for (int kb = 0; kb < p.nkb; kb += KPS) {
-        if (__any_sync(0xFFFFFFFFu, !mbar_wait(&full_bar[stage], phase, &abort_flag))) { stop = true; break; }
+    // one lane runs the loop (no warp-wide step in it); the warp meets again
+    // behind it
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      bool issued = false;
+      bool stop = false;
+      int i = 0;
+      for (int t = blockIdx.x; t < total && !stop; t += gridDim.x, ++i) {
+        const int acc = i & 1;
+        const uint32_t acc_phase = (i >> 1) & 1;
+        if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, &abort_flag)) break;
         tc_fence_after();
-        if (lane == 0) {
+        const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAccStride;
+        for (int kb = 0; kb < p.nkb; kb += KPS) {
+          if (!mbar_wait(&full_bar[stage], phase, &abort_flag)) { stop = true; break; }
+          tc_fence_after();
           const int nsub = min(KPS, p.nkb - kb);
           for (int u = 0; u < nsub; ++u) {
             const uint64_t ad = smem_desc(smem_u32(sA + (stage * KPS + u) * kABytes));
@@ -792,18 +794,16 @@ __global__ void __launch_bounds__(gemm_threads<ACT>(), 1)
           }
           tc_commit(&empty_bar[stage]);
           issued = true;
+          if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
-        __syncwarp();
-        if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+        if (stop) break;
+        tc_commit(&tfull_bar[acc]);
       }
-      if (stop) break;
-      if (lane == 0) tc_commit(&tfull_bar[acc]);
-      __syncwarp();
-    }
-    if (abort_flag && lane == 0 && issued) {
-      int dummy = 0;
-      tc_commit(&final_bar);
-      mbar_wait(&final_bar, 0, &dummy, kDrainLimitNs);
+      if (abort_flag && issued) {
+        int dummy = 0;
+        tc_commit(&final_bar);
+        mbar_wait(&final_bar, 0, &dummy, kDrainLimitNs);
+      }
     }
     __syncwarp();
   } else {
@@ -1250,7 +1250,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<ACT>(),
       }
     }
   } else if (warp == 1) {
-    if (leader) {
+    if (leader && lane == 0) {
       // ------------------------------------------------------- MMA issuer
       int stage = 0;
       uint32_t phase = 0;
@@ -1260,41 +1260,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(gemm_threads<ACT>(),
       for (int t = cluster; t < total && !stop; t += nclusters, ++i) {
         const int acc = i % kAccs;
         const uint32_t acc_phase = (i / kAccs) & 1;
-        // the warp agrees on giving up a wait, so that no lane is left at a
-        // warp-wide step after another has left
-        if (__any_sync(0xFFFFFFFFu, !mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, &abort_flag))) break;
+        if (!mbar_wait(&tempty_bar[acc], acc_phase ^ 1u, &abort_flag)) break;
         tc_fence_after();
         const uint32_t d_tmem = tmem_base + static_cast<uint32_t>(acc) * kAccStride;
         for (int kb = 0; kb < p.nkb; ++kb) {
-          if (__any_sync(0xFFFFFFFFu, !mbar_wait(&full_bar[stage], phase, &abort_flag))) { stop = true; break; }
+          if (!mbar_wait(&full_bar[stage], phase, &abort_flag)) { stop = true; break; }
           tc_fence_after();
-          if (lane == 0) {
-            const uint64_t ad = smem_desc(smem_u32(sA + stage * kABytes));
+          const uint64_t ad = smem_desc(smem_u32(sA + stage * kABytes));
 #pragma unroll
-            for (int k = 0; k < kBKBytes / 32; ++k)
+          for (int k = 0; k < kBKBytes / 32; ++k)
 #pragma unroll
-              for (int s = 0; s < NSUB; ++s) {
-                const uint64_t bd = smem_desc(smem_u32(sB + stage * kBBytes + s * kBSub));
-                mma_issue_pair<KIND>(d_tmem + static_cast<uint32_t>(SUBN * s), ad + 2u * k, bd + 2u * k, p.idesc,
-                                     (kb > 0 || k > 0) ? 1u : 0u);
-              }
-            tc_commit_pair(&empty_bar[stage]);
-            issued = true;
-          }
-          __syncwarp();
+            for (int s = 0; s < NSUB; ++s) {
+              const uint64_t bd = smem_desc(smem_u32(sB + stage * kBBytes + s * kBSub));
+              mma_issue_pair<KIND>(d_tmem + static_cast<uint32_t>(SUBN * s), ad + 2u * k, bd + 2u * k, p.idesc,
+                                   (kb > 0 || k > 0) ? 1u : 0u);
+            }
+          tc_commit_pair(&empty_bar[stage]);
+          issued = true;
           if (++stage == STAGES) { stage = 0; phase ^= 1u; }
         }
         if (stop) break;
-        if (lane == 0) tc_commit_pair(&tfull_bar[acc]);
-        __syncwarp();
+        tc_commit_pair(&tfull_bar[acc]);
       }
-      if (abort_flag && lane == 0 && issued) {
+      if (abort_flag && issued) {
         int dummy = 0;
         tc_commit(&final_bar);
         mbar_wait(&final_bar, 0, &dummy, kDrainLimitNs);
       }
-      __syncwarp();
     }
+    __syncwarp();
   } else {
     // -------------------------------------------------------- epilogue
     // Eight warps: warp w reads TMEM lane quadrant w % 4 (32 rows of this
@@ -1548,7 +1542,12 @@ cudaError_t dispatch_gemm(const GemmArgs& a, std::string* msg) {
   }
   if (a.kind == 0) {
     if (wide) return run<0, 256, 4, kBM, 1, ACT>(a, msg);
-    return run<0, 128, 6, kBM, 1, ACT>(a, msg);
+    // three K blocks per stage: a stage's hand-over (wait, commit, refill)
+    // costs the issuer some 235 cycles against 256 of MMA per block
+    // (M = 2047, N = 1024, K = 4096: 13.2 us against 15.8 with six stages of
+    // one); the grouped form prefetches block by block and keeps those
+    if (a.offsets == nullptr) return run<0, 128, 2, kBM, 3, ACT>(a, msg);
+    return run<0, 128, 6>(a, msg);
   }
   if (wide) return run<1, 256, 4>(a, msg);
   return run<1, 128, 6>(a, msg);
