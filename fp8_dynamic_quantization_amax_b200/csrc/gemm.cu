@@ -396,29 +396,37 @@ __device__ __forceinline__ uint4 ld_global_v4(const void* p) {
 // finite |z|, m = fmax / amax (1 when amax is 0 or the quotient is not
 // finite), saturating RNE, NaN -> 0x7F.  z is quantized in f32, without the
 // bf16 rounding that a stored result takes: the codes are rounded once.
-__device__ __forceinline__ float chunk_f32_to_fp8(const float (&z)[32], int fmt, uint32_t (&c4)[8]) {
-  uint32_t mx = 0;
+template <int FMT, bool EXACT>
+__device__ __forceinline__ void chunk_codes(const float (&z)[32], float m, uint32_t (&c4)[8]) {
+  const float2 m2 = make_float2(m, m);
 #pragma unroll
-  for (int j = 0; j < 32; ++j) mx = max(mx, __float_as_uint(z[j]) & 0x7FFFFFFFu);
-  const bool special = mx >= 0x7F800000u;
-  if (special) {
-    mx = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j) mx = max(mx, __float_as_uint(finite_abs(z[j])));
+  for (int j = 0; j < 16; ++j) {
+    const float2 t = f2_mul(make_float2(z[2 * j], z[2 * j + 1]), m2);
+    const uint32_t c2 = EXACT ? cvt2_exact<FMT>(t.x, t.y) : cvt2_fast<FMT>(t.x, t.y);
+    c4[j >> 1] = (j & 1) ? (c4[j >> 1] | (c2 << 16)) : c2;
   }
-  const float a = __uint_as_float(mx);
+}
+__device__ __forceinline__ float chunk_f32_to_fp8(const float (&z)[32], int fmt, uint32_t (&c4)[8]) {
+  float a = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) a = max3_abs_nan(a, z[2 * j], z[2 * j + 1]);
+  const bool special = !(a <= FLT_MAX);
+  if (special) {
+    a = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) a = fmaxf(a, finite_abs(z[j]));
+  }
   float m = 1.0f;
   if (a > 0.0f) {
     m = __fdiv_rn(fmt == 0 ? kFmaxE4M3 : kFmaxE5M2, a);
     if (!(m <= FLT_MAX)) m = 1.0f;
   }
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float lo = __fmul_rn(z[2 * j], m), hi = __fmul_rn(z[2 * j + 1], m);
-    uint32_t c2;
-    if (special) c2 = (fmt == 0) ? cvt2_exact<0>(lo, hi) : cvt2_exact<1>(lo, hi);
-    else c2 = (fmt == 0) ? cvt2_fast<0>(lo, hi) : cvt2_fast<1>(lo, hi);
-    c4[j >> 1] = (j & 1) ? (c4[j >> 1] | (c2 << 16)) : c2;
+  if (special) {
+    if (fmt == 0) chunk_codes<0, true>(z, m, c4);
+    else chunk_codes<1, true>(z, m, c4);
+  } else {
+    if (fmt == 0) chunk_codes<0, false>(z, m, c4);
+    else chunk_codes<1, false>(z, m, c4);
   }
   return m;
 }
