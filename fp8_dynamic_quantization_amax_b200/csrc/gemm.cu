@@ -1564,7 +1564,8 @@ cudaError_t dispatch_gemm(const GemmArgs& a, std::string* msg) {
 }  // namespace
 
 cudaError_t launch_gemm(const GemmArgs& a, std::string* msg) {
-  return a.act_epilogue ? dispatch_gemm<true>(a, msg) : dispatch_gemm<false>(a, msg);
+  if (!a.act_epilogue) return dispatch_gemm<false>(a, msg);
+  return gemm_decode_takes(a) ? launch_gemm_decode(a, msg) : dispatch_gemm<true>(a, msg);
 }
 
 unsigned* device_error_word() {

@@ -1,6 +1,6 @@
 // hq_internal.cuh -- declarations shared by the translation units of
-// libhq.so (api.cu, quantize.cu, gemm.cu, gemm_bs.cu, grad_bias.cu, norm.cu,
-// act_bwd.cu, noalloc.cu, probe.cu).
+// libhq.so (api.cu, quantize.cu, gemm.cu, gemm_bs.cu, gemm_decode.cu,
+// grad_bias.cu, norm.cu, act_bwd.cu, noalloc.cu, probe.cu).
 // Not part of the public ABI.
 #pragma once
 
@@ -165,6 +165,11 @@ struct GemmArgs {
   int z_fmt = 0;
   float* z_scales = nullptr;      // [M, N / 32]
 };
+
+// The activation epilogue's GEMM for few rows and columns, split over K in a
+// cluster (gemm_decode.cu), and whether it takes a call.
+bool gemm_decode_takes(const GemmArgs& a);
+cudaError_t launch_gemm_decode(const GemmArgs& a, std::string* msg);
 
 // Returns cudaSuccess or the failing call's error; *msg gets a description.
 cudaError_t launch_gemm(const GemmArgs& a, std::string* msg);

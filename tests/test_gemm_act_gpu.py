@@ -61,9 +61,9 @@ def check(out, z, err, act, res):
     assert bool((off <= tol).all()), "%d off, worst %g of its bound" % (int((off > tol).sum()), float((off / tol).max()))
 
 
-# up to 16 rows: one group of columns, more than the SMs, several batches, K of one step, an odd number and many
-SHAPES += [(1, 8, 64), (2, 16, 16), (4, 1184, 1040), (7, 10056, 208), (8, 20000, 1024), (9, 40, 8192), (12, 3000, 2064),
-           (15, 28680, 128), (16, 8192, 28672)]
+# up to 16 rows, K split over clusters of 8, 4 and 2: fewer K blocks than CTAs, an uneven split, ragged tiles of columns
+SHAPES += [(1, 8, 64), (2, 16, 16), (4, 1184, 1040), (7, 2056, 208), (8, 4104, 1024), (9, 40, 8192), (12, 3000, 2064),
+           (15, 9480, 1168), (16, 8192, 28672), (11, 1024, 4096), (16, 9472, 2048), (5, 18952, 400)]
 
 
 @pytest.mark.parametrize("shape", SHAPES, ids=str)
