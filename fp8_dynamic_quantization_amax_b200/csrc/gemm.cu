@@ -32,6 +32,7 @@
 #include <cuda_bf16.h>
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
@@ -1002,16 +1003,29 @@ void set_fused_epilogue(const GemmArgs& a, Params& p) {
   p.wide = at32(a.out) && at32(a.residual) && a.N % 16 == 0 && (a.z_q == nullptr || at32(a.z_q));
 }
 
+// Runs set-up (a kernel's attributes, which belong to a device) on its first
+// call on each device; one set of flags per set-up, that is per kernel.
+template <typename F>
+cudaError_t once_per_device(F set_up) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = set_up();
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int KIND, int BN, int STAGES, int AROWS = kBM, int KPS = 1, bool ACT = false>
 cudaError_t run(const GemmArgs& a, std::string* msg) {
   constexpr int kElem = (KIND == 0) ? 1 : 2;
   constexpr int kSmem = STAGES * KPS * (AROWS + BN) * kBKBytes + epi_smem<ACT>((BN + 31) / 32) + 1024;
   static_assert(kSmem + 8352 <= 232448, "shared memory over the 227 KB per-CTA limit");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err =
-        cudaFuncSetAttribute(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  const cudaError_t attr_err = once_per_device([] {
+    return cudaFuncSetAttribute(k_gemm<KIND, BN, STAGES, AROWS, KPS, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                kSmem);
   });
   if (attr_err != cudaSuccess) {
     *msg = "cudaFuncSetAttribute failed";
@@ -1415,13 +1429,11 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   constexpr int kSmem =
       STAGES * (128 + BN / 2) * kBKBytes + epi_smem<ACT>(BN / 32) + 1024;
   static_assert(kSmem + 8400 <= 232448, "shared memory over the 227 KB per-CTA limit");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;
-  std::call_once(once, [] {
-    attr_err =
-        cudaFuncSetAttribute(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr_err != cudaSuccess) return;
+  static std::atomic<int> max_clusters{0};  // the same on every B200
+  const cudaError_t attr_err = once_per_device([] {
+    const cudaError_t e = cudaFuncSetAttribute(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(148, 1, 1);
     cfg.blockDim = dim3(gemm_threads<ACT>(), 1, 1);
@@ -1433,10 +1445,13 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
     attr.val.clusterDim.z = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&max_clusters, k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, &cfg) != cudaSuccess) {
+    int fit = 0;
+    if (cudaOccupancyMaxActiveClusters(&fit, k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, &cfg) != cudaSuccess) {
       cudaGetLastError();
-      max_clusters = 0;
+      fit = 0;
     }
+    max_clusters = fit;
+    return cudaSuccess;
   });
   if (attr_err != cudaSuccess) {
     *msg = "cudaFuncSetAttribute failed";
@@ -1481,7 +1496,7 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   int dev = 0;
   cudaGetDevice(&dev);
   int clusters = device_sm_count(dev) / 2;
-  if (max_clusters > 0 && max_clusters < clusters) clusters = max_clusters;
+  if (max_clusters > 0 && max_clusters < clusters) clusters = max_clusters.load();
   // grouped: the tile count lives on the device; a bound suffices
   const int64_t tiles = static_cast<int64_t>(p.m_tiles + (a.offsets != nullptr ? a.E : 0)) * p.n_tiles;
   if (tiles < clusters) clusters = static_cast<int>(tiles);

@@ -138,3 +138,40 @@ def test_decode_step_of_one_token():
         # another tile adds the products in another grouping: the same value within the accumulation's error
         torch.cuda.synchronize()
         assert float((a.float() - s["a"][r:r + 1].float()).abs().max()) <= 2.0 ** -7 * float(s["a"][r].float().abs().max())
+
+
+FIRST_CALLS = """
+import torch
+import fp8_dynamic_quantization_amax_b200 as H
+n = lambda *s: torch.randn(s, device="cuda").bfloat16()
+x, w, rstd = n(64, 1024), n(1024), torch.rand(64, device="cuda")
+q = torch.randint(0, 100, (64, 1024), dtype=torch.uint8, device="cuda")
+wq = torch.randint(0, 100, (2048, 1024), dtype=torch.uint8, device="cuda")
+one, zs = torch.ones(1, device="cuda"), torch.rand(64, 32, device="cuda")
+
+def calls():
+    return [*H.hq_rmsnorm_fp8(x, w, 1e-5)[:2], *H.hq_rmsnorm_backward(x, x, w, rstd), *H.hq_act_backward_fp8(x, q, zs, 2),
+            H.hq_gemm_a8w8_act(q, wq, one, one, act=2), H.hq_gemm_a8w8_act(q[:3], wq, one, one, act=2)]
+
+torch.cuda.synchronize()
+gr = torch.cuda.CUDAGraph()
+with torch.cuda.graph(gr):
+    got = calls()
+gr.replay()
+torch.cuda.synchronize()
+again = calls()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(got, again))
+H.hq_check_device_error()
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture():
+    # kernels set up and loaded while a stream is being captured
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "same", r.stderr[-2000:]

@@ -178,3 +178,40 @@ def test_captured_graphs_and_another_stream():
     torch.cuda.synchronize()
     for a, b, c in zip(want, other, got):
         assert torch.equal(a, b) and torch.equal(a, c)
+
+
+@pytest.mark.parametrize("shape", [(1, 8192, 1024), (16, 1024, 4096), (5, 4096, 400)], ids=str)
+def test_decode_calls_on_two_streams_at_once(shape):
+    # cluster launches of two graphs interleaved on two streams, the residual stream updated in place by each
+    xq, wq, xs, ws, bias, res = operands(*shape, seed=5)
+    want = H.hq_gemm_a8w8_act(xq, wq, xs, ws, bias=bias, act=H.ACT_GELU, residual=res)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    graphs, streams = [], [res.clone(), res.clone()]
+    for s in streams:
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            s.copy_(res)
+            H.hq_gemm_a8w8_act(xq, wq, xs, ws, bias=bias, act=H.ACT_GELU, residual=s, out=s)
+        graphs.append(gr)
+    for _ in range(20):
+        graphs[0].replay()
+        with torch.cuda.stream(side):
+            graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(streams[0], want) and torch.equal(streams[1], want)
+    H.hq_check_device_error()
+
+
+def test_scales_and_bias_off_the_vector_grid():
+    # column scales and bias that start 4 bytes off a 16-byte boundary, rows of out 16 bytes off a 32-byte one
+    for M, N, K in ((3, 1024, 256), (40, 520, 64), (200, 264, 256), (700, 2048, 128)):
+        xq, wq, xs, ws, bias, res = operands(M, N, K, seed=N)
+        z, err = plain(xq, wq, xs, ws, bias)
+        ws1 = torch.empty(N + 1, device="cuda")[1:].copy_(ws)
+        bias1 = torch.empty(N + 2, dtype=torch.bfloat16, device="cuda")[2:].copy_(bias)
+        out = torch.empty(M * N + 8, dtype=torch.bfloat16, device="cuda")[8:].view(M, N)
+        res1 = torch.empty(M * N + 8, dtype=torch.bfloat16, device="cuda")[8:].view(M, N).copy_(res)
+        H.hq_gemm_a8w8_act(xq, wq, xs, ws1, bias=bias1, act=H.ACT_SILU, residual=res1, out=out)
+        torch.cuda.synchronize()
+        check(out, z, err, H.ACT_SILU, res)
