@@ -163,7 +163,8 @@ __global__ void __launch_bounds__(kAnyThreads) k_rmsnorm_any(const NormParams p)
 // so the refill needs no barrier of its own.
 //
 // Block-wise scales: a block of 16-byte vectors that is a power of two up to
-// 32 lies inside one warp's consecutive lanes, so its maximum is a shuffle.
+// 32 lies inside one warp's consecutive lanes, so its maximum is a shuffle, and
+// its lanes share out the divisions of the blocks that they hold.
 constexpr int kRingStages = 8;
 // Elements per thread.  Most rows run with 16 or 24 elements and the weight
 // in registers, up to 512 threads of 128 registers per SM: measured on
@@ -397,26 +398,47 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
       amax = __uint_as_float(join_max(sh.top[par], warps));
     }
     if (tid == 0 && p.rstd_out) p.rstd_out[row] = rstd;
-    float m = 1.0f;
+    float m[ITEMS];
     if (group == 0) {
-      m = multiplier_of(amax, p.fmt);
-      if (tid == 0) p.scales[row] = __fdiv_rn(1.0f, m);
+      m[0] = multiplier_of(amax, p.fmt);
+      if (tid == 0) p.scales[row] = __fdiv_rn(1.0f, m[0]);
+#pragma unroll
+      for (int it = 1; it < ITEMS; ++it) m[it] = m[0];
+    } else {
+      for (int o = 1; o < group; o <<= 1) {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) vtop[it] = fmaxf(vtop[it], __shfl_xor_sync(0xFFFFFFFFu, vtop[it], o));
+      }
+      float* srow = p.scales + static_cast<int64_t>(row) * p.nb;
+      const int in = lane & (group - 1);
+      if (group >= ITEMS) {  // lane `in` of a group divides for the group's block of item `in`
+        float mine = vtop[0];
+#pragma unroll
+        for (int it = 1; it < ITEMS; ++it) mine = in == it ? vtop[it] : mine;
+        const float mb = multiplier_of(special ? mine : __fmul_rn(mine, rstd), p.fmt);
+        const float inv = __fdiv_rn(1.0f, mb);
+        const int v = in * T + tid;
+        if (in < ITEMS && v - in < nv) srow[v >> group_log] = inv;
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) m[it] = __shfl_sync(0xFFFFFFFFu, mb, lane - in + it);
+      } else {
+#pragma unroll
+        for (int it = 0; it < ITEMS; ++it) {
+          const int v = it * T + tid;
+          m[it] = multiplier_of(special ? vtop[it] : __fmul_rn(vtop[it], rstd), p.fmt);
+          if (in == 0 && v < nv) srow[v >> group_log] = __fdiv_rn(1.0f, m[it]);
+        }
+      }
     }
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       const int v = it * T + tid;
-      if (group != 0) {
-        float bt = vtop[it];
-        for (int o = 1; o < group; o <<= 1) bt = fmaxf(bt, __shfl_xor_sync(0xFFFFFFFFu, bt, o));
-        m = multiplier_of(special ? bt : __fmul_rn(bt, rstd), p.fmt);
-        if (v < nv && (lane & (group - 1)) == 0) p.scales[static_cast<int64_t>(row) * p.nb + (v >> group_log)] = __fdiv_rn(1.0f, m);
-      }
       if (v < nv) {
         const int64_t at = static_cast<int64_t>(row) * p.cols + v * VEC;
         const float2* y = h + it * (VEC / 2);
         if (p.y_out)
           vec_store(static_cast<char*>(p.y_out) + at * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(y)));
-        store_codes<VEC>(p.q + at, y, m, p.fmt, special);
+        store_codes<VEC>(p.q + at, y, m[it], p.fmt, special);
       }
     }
     if (++stage == stages) { stage = 0; phase ^= 1u; }
