@@ -315,3 +315,69 @@ def test_another_stream_and_a_captured_graph():
     for o in outs:
         for a, b in zip(o, (q, s, h, dx, dw)):
             assert torch.equal(a, b)
+
+
+# --------------------------- widths that are not a whole number of vectors
+# (rows that share their first and last 16 bytes with their neighbours)
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("rows,cols", [(2003, 1001), (1301, 257), (900, 4099), (150, 8191), (149, 12291), (5001, 25),
+                                       (333, 100), (2401, 1004), (148, 8189), (301, 16369), (7, 24), (1, 1002)])
+def test_rows_between_vectors(rows, cols, dtype):
+    wdtype = torch.float32 if rows % 2 else dtype
+    x, w, r = inputs(rows, cols, dtype, wdtype, True, seed=cols)
+    for res in (r, None):
+        guard = lambda dt: torch.full((rows * cols + 64,), 77, dtype=dt, device="cuda")  # noqa: E731
+        view = lambda b: b[:rows * cols].view(rows, cols)  # noqa: E731
+        qb, yb, hb = guard(torch.uint8), guard(dtype), guard(dtype)
+        rstd = torch.empty(rows, device="cuda")
+        q, s, h = H.hq_rmsnorm_fp8(x, w, 1e-5, residual=res, q=view(qb), y_out=view(yb), rstd_out=rstd,
+                                   residual_out=view(hb) if res is not None else None)
+        torch.cuda.synchronize()
+        check_forward(x, w, res, 1e-5, H.E4M3, 0, q, s, h if res is not None else None, view(yb), rstd)
+        assert all(bool((b[rows * cols:] == 77).all()) for b in (qb, yb, hb))
+    x2 = x.clone()
+    q2, s2, h2 = H.hq_rmsnorm_fp8(x2, w, 1e-5, residual=r, residual_out=x2)
+    q1, s1, h1 = H.hq_rmsnorm_fp8(x, w, 1e-5, residual=r)
+    torch.cuda.synchronize()
+    assert torch.equal(q1, q2) and torch.equal(s1, s2) and torch.equal(h1, h2)
+
+
+@pytest.mark.parametrize("dtype,wdtype", [(torch.bfloat16, torch.float32), (torch.float16, torch.float16),
+                                          (torch.float32, torch.float32)])
+@pytest.mark.parametrize("rows,cols", [(2003, 1001), (1301, 257), (777, 4099), (150, 8191), (149, 12291), (5001, 25),
+                                       (333, 100), (2401, 1004), (301, 16369), (7, 24), (1, 1002)])
+def test_backward_of_rows_between_vectors(rows, cols, dtype, wdtype):
+    for with_dres in (False, True):
+        h, w, dres = inputs(rows, cols, dtype, wdtype, with_dres, seed=rows)
+        dy, _, _ = inputs(rows, cols, dtype, wdtype, False, seed=rows + 1)
+        rstd = (h.float().square().mean(1) + 1e-5).rsqrt()
+        buf = torch.full((rows * cols + 64,), 77, dtype=dtype, device="cuda")
+        dx, dw = H.hq_rmsnorm_backward(dy, h, w, rstd, dres=dres, dx=buf[:rows * cols].view(rows, cols))
+        torch.cuda.synchronize()
+        check_backward(dy, h, w, rstd, dres, dx, dw)
+        assert bool((buf[rows * cols:] == 77).all())
+        dx2, dw2 = H.hq_rmsnorm_backward(dy, h, w, rstd, dres=dres)
+        torch.cuda.synchronize()
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("cols", [1001, 4098, 60])
+def test_neighbouring_rows_do_not_mix(cols, dtype):
+    # rows of NaN leave the rows that share their vectors as they are
+    rows = 997
+    x, w, r = inputs(rows, cols, dtype, dtype, True, seed=12)
+    q, s, h = H.hq_rmsnorm_fp8(x, w, 1e-5, residual=r)
+    rstd = torch.rand(rows, device="cuda") + 0.5
+    dx, _ = H.hq_rmsnorm_backward(x, r, w, rstd, dres=x)
+    bad = torch.zeros(rows, dtype=torch.bool, device="cuda")
+    bad[1::3] = True
+    bad[-1] = False
+    x2 = x.clone()
+    x2[bad] = float("nan")
+    q2, s2, h2 = H.hq_rmsnorm_fp8(x2, w, 1e-5, residual=r)
+    dx2, _ = H.hq_rmsnorm_backward(x2, r, w, rstd, dres=x)
+    torch.cuda.synchronize()
+    for a, b in ((q, q2), (s, s2), (h, h2), (dx, dx2)):
+        assert torch.equal(a[~bad], b[~bad])
+    assert bool((q2[bad] == 0x7F).all()) and bool(torch.isnan(dx2[bad]).all())
