@@ -57,14 +57,6 @@ struct DecodeParams {
   unsigned* err;
 };
 
-__device__ __forceinline__ uint32_t cluster_rank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
 // a float at shared-memory address addr of CTA rank of the cluster
 __device__ __forceinline__ float load_cluster(uint32_t addr, uint32_t rank) {
   float f;
@@ -100,7 +92,7 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kDkThreads, 1)
   uint8_t* sA = smem_raw + ((1024u - (raw & 1023u)) & 1023u);
   uint8_t* sB = sA + kDkStages * kDkBlocks * kDkA;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t rank = cluster_rank();
+  const uint32_t rank = ptx::cluster_rank();
   const int col0 = static_cast<int>(blockIdx.x / S) * p.width;
   const int k0 = static_cast<int>(static_cast<int64_t>(rank) * p.nkb / S);  // this CTA's K blocks
   const int k1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.nkb / S);
@@ -208,9 +200,8 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kDkThreads, 1)
       tc_fence_before();
     }
   }
-  __syncwarp();
   tc_fence_before();
-  cluster_barrier();  // every CTA's partial sums are in its shared memory
+  ptx::cluster_barrier();  // every CTA's partial sums are in its shared memory
   if (warp == 1) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(static_cast<uint32_t>(kDkCols))
@@ -247,8 +238,7 @@ __global__ void __cluster_dims__(S, 1, 1) __launch_bounds__(kDkThreads, 1)
       *reinterpret_cast<uint32_t*>(p.out + at) = pack_bf16x2(z0, z1);
     }
   }
-  __syncwarp();
-  cluster_barrier();  // no CTA leaves while another may still read its sums
+  ptx::cluster_barrier();  // no CTA leaves while another may still read its sums
 }
 
 template <int S>

@@ -174,11 +174,15 @@ constexpr int kRingStages = 8;
 // took 148 us, held to 64 registers with two CTAs 171 us (the compiler then
 // orders the loads behind one another), 32 elements in two CTAs of 256
 // threads 171 us, in one 190 us; the backward pass 158, 180, 165 and 164 us.
-// Eight elements serve a single row per CTA (latency) and narrow rows; rows
-// beyond 16384 columns hold 32 elements in up to 1024 threads and read the
-// weight per row.
+// Eight elements serve a single row per CTA (latency) and narrow rows.
+//
+// Rows beyond the columns or the stages of one CTA are split over a cluster
+// (CL): every CTA a run of the row's vectors, the warps' sums and maxima
+// written into all its CTAs' shared memories, a cluster barrier in place of
+// the block's.
 constexpr int kRingMaxCols = 16384;
-constexpr int ring_max_threads(int e, bool wide) { return (e == 8 || wide) ? 1024 : 512; }
+constexpr int ring_max_threads(int e) { return e == 8 ? 1024 : 512; }
+constexpr int kRingSlots = 64;  // warps of a CTA or cluster
 
 template <int XT>
 constexpr int vec_elems() {
@@ -189,13 +193,21 @@ template <int VEC>
 __host__ __device__ constexpr uint32_t shifted_vecs(int cols) {
   return static_cast<uint32_t>((cols + 2 * VEC - 2) / VEC);
 }
+// vectors of a row per CTA of its cluster: whole blocks of scales in each
+template <int VEC, bool SHIFT>
+__host__ __device__ constexpr int cluster_share(int cols, int ctas) {
+  const int all = SHIFT ? static_cast<int>(shifted_vecs<VEC>(cols)) : cols / VEC;
+  return ((all + ctas - 1) / ctas + 31) / 32 * 32;
+}
 
 struct RingShared {
   uint64_t full[kRingStages];
-  float sum[2][32];       // by row parity, per warp
-  uint32_t top[2][32];
+  float sum[2][kRingSlots];       // by row parity, per warp of the CTA (or cluster)
+  uint32_t top[2][kRingSlots];
   int abort_flag;
 };
+
+constexpr uint32_t kGaveUp = 0xFFFFFFFFu;  // above every maximum's bits
 
 __device__ __forceinline__ void ring_init(RingShared& sh, int stages) {
   if (threadIdx.x == 0) {
@@ -220,14 +232,20 @@ __device__ __forceinline__ void drain_stages(uint64_t* full, int stages, int sta
   } while (stage != next_stage);
 }
 
-// this warp's lanes' values joined over all warps of the CTA (after the barrier)
+// the warps' values joined (after the barrier); CL: up to 64 of them
+template <bool CL>
 __device__ __forceinline__ float join_sum(const float* red, int warps) {
   const int lane = threadIdx.x & 31;
-  return warp_sum(lane < warps ? red[lane] : 0.0f);
+  float v = lane < warps ? red[lane] : 0.0f;
+  if (CL && lane + 32 < warps) v += red[lane + 32];
+  return warp_sum(v);
 }
+template <bool CL>
 __device__ __forceinline__ uint32_t join_max(const uint32_t* red, int warps) {
   const int lane = threadIdx.x & 31;
-  return __reduce_max_sync(0xFFFFFFFFu, lane < warps ? red[lane] : 0u);
+  uint32_t v = lane < warps ? red[lane] : 0u;
+  if (CL && lane + 32 < warps) v = max(v, red[lane + 32]);
+  return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
 // VEC weights from column c as f32 (16-byte aligned weight, c a multiple of VEC)
@@ -312,30 +330,37 @@ __device__ __forceinline__ void codes(uint32_t (&c)[VEC / 4], const float2* y, f
   }
 }
 
-template <int XT, int E, bool RES, bool WIDE, bool SHIFT>
-__global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(const NormParams p, const int stages, unsigned* err) {
+template <int XT, int E, bool RES, bool SHIFT, bool CL>
+__global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const NormParams p, const int stages, unsigned* err) {
   constexpr int VEC = vec_elems<XT>();
   constexpr int ITEMS = E / VEC;
-  constexpr bool kWeightRegs = !WIDE;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ RingShared sh;
   const int tid = threadIdx.x, T = blockDim.x;
   const int warp = tid >> 5, lane = tid & 31, warps = T >> 5;
+  const int ctas = CL ? static_cast<int>(ptx::cluster_size()) : 1, rank = CL ? static_cast<int>(ptx::cluster_rank()) : 0;
+  const int first = CL ? static_cast<int>(blockIdx.x) / ctas : static_cast<int>(blockIdx.x);
+  const int stride = CL ? static_cast<int>(gridDim.x) / ctas : static_cast<int>(gridDim.x);
   // columns before the row in its first vector; the same for all rows of a CTA
-  const int shift = SHIFT ? static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.cols % VEC) : 0;
-  const int nv = (shift + p.cols + VEC - 1) / VEC;
-  const uint32_t row_bytes = SHIFT ? shifted_vecs<VEC>(p.cols) * 16u : static_cast<uint32_t>(nv) * 16u;  // room in a stage
+  const int shift = SHIFT ? static_cast<int>(static_cast<int64_t>(first) * p.cols % VEC) : 0;
+  const int all = (shift + p.cols + VEC - 1) / VEC;
+  const int share = CL ? cluster_share<VEC, SHIFT>(p.cols, ctas) : all;  // vectors per CTA
+  const int nv = CL ? max(0, min(share, all - rank * share)) : all;
+  const int col0 = (CL ? rank * share * VEC : 0) - shift;  // this CTA's first column
+  const int slots = (T >> 5) * ctas;
+  // room in a stage
+  const uint32_t row_bytes = CL ? share * 16u : SHIFT ? shifted_vecs<VEC>(p.cols) * 16u : static_cast<uint32_t>(nv) * 16u;
   const uint32_t stage_bytes = row_bytes * (RES ? 2 : 1);
   const int64_t total = static_cast<int64_t>(p.rows) * p.cols;
   ring_init(sh, stages);
+  if (CL) ptx::cluster_barrier();  // all CTAs of the cluster are there to be written to
   pdl_wait();
   pdl_launch_dependents();
-  const int stride = static_cast<int>(gridDim.x);
-  int next = static_cast<int>(blockIdx.x);  // thread 0: the next row to bring in, and its stage
+  int next = first;  // thread 0: the next row to bring in, and its stage
   int next_stage = 0;
   auto issue = [&] {
     const int s = next_stage;
-    const int64_t at = static_cast<int64_t>(next) * p.cols - shift;  // a multiple of VEC
+    const int64_t at = static_cast<int64_t>(next) * p.cols + col0;  // a multiple of VEC
     // whole vectors inside the tensor
     const uint32_t bytes = (SHIFT && at + static_cast<int64_t>(nv) * VEC > total ? nv - 1 : nv) * 16u;
     ptx::mbar_arrive_expect_tx(&sh.full[s], bytes * (RES ? 2 : 1));
@@ -349,16 +374,14 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
   if (tid == 0)
     for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
-  float2 w[kWeightRegs ? E / 2 : 1];
-  if (kWeightRegs) {
+  float2 w[E / 2];
 #pragma unroll
-    for (int it = 0; it < ITEMS; ++it) {
-      const int v = it * T + tid;
-      if (v < nv) {
-        float* wv = reinterpret_cast<float*>(w + (kWeightRegs ? it * (VEC / 2) : 0));
-        if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, v * VEC - shift, p.cols, wv);
-        else load_weight<VEC>(p.weight, p.wt, v * VEC, wv);
-      }
+  for (int it = 0; it < ITEMS; ++it) {
+    const int v = it * T + tid;
+    if (v < nv) {
+      float* wv = reinterpret_cast<float*>(w + it * (VEC / 2));
+      if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, col0 + v * VEC, p.cols, wv);
+      else load_weight<VEC>(p.weight, p.wt, col0 + v * VEC, wv);
     }
   }
   const int group = p.block ? p.block / VEC : 0;  // lanes per block, a power of two
@@ -366,12 +389,13 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
   int stage = 0;
   uint32_t phase = 0;
   int par = 0;
-  for (int row = static_cast<int>(blockIdx.x); row < p.rows; row = p.rows - row > stride ? row + stride : p.rows) {
+  bool quit = false;
+  for (int row = first; row < p.rows; row = p.rows - row > stride ? row + stride : p.rows) {
     const bool ok = ptx::mbar_wait_inline(&sh.full[stage], phase, &sh.abort_flag, err, kDevErrTimeout);
     const uint4* xs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
     const uint4* rs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
     const int64_t row_at = static_cast<int64_t>(row) * p.cols;
-    const bool cut = SHIFT && row_at - shift + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
+    const bool cut = SHIFT && row_at + col0 + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
     // every vector is asked for before the first is used
     uint4 xr[ITEMS], rr[RES ? ITEMS : 1];
 #pragma unroll
@@ -391,7 +415,7 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
       float2* hv = h + it * (VEC / 2);
       vtop[it] = 0.0f;
       if (v < nv) {
-        const int c0 = v * VEC - shift;
+        const int c0 = col0 + v * VEC;
         const bool edge = SHIFT && is_edge<VEC>(c0, p.cols);
         if (SHIFT && edge) widen_edge<XT, VEC>(xr[it], p.x, row_at, c0, p.cols, cut && v == nv - 1, reinterpret_cast<float*>(hv));
         else vec_widen<XT>(xr[it], reinterpret_cast<float*>(hv));
@@ -411,12 +435,10 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
                         vec_narrow<XT>(reinterpret_cast<const float*>(hv)));
           }
         }
-        float2 wl[VEC / 2];
-        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
           ss2 = f2_fma(hv[j], hv[j], ss2);
-          hv[j] = f2_mul(hv[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]);  // h w from here on
+          hv[j] = f2_mul(hv[j], w[it * (VEC / 2) + j]);  // h w from here on
           vtop[it] = max3_abs_nan(vtop[it], hv[j].x, hv[j].y);
         }
         top = max3_abs_nan(top, vtop[it], 0.0f);
@@ -427,14 +449,30 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
     }
     float ss = warp_sum(ss2.x + ss2.y);
     const uint32_t wtop = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(top));  // NaN's bits are above infinity's
-    if (lane == 0) {
-      sh.sum[par][warp] = ss;
-      sh.top[par][warp] = wtop;
+    if (CL) {
+      const bool gave_up = __any_sync(0xFFFFFFFFu, !ok);
+      if (lane < ctas) {
+        const int slot = rank * warps + warp;
+        ptx::store_cluster(&sh.sum[par][slot], lane, __float_as_uint(ss));
+        ptx::store_cluster(&sh.top[par][slot], lane, gave_up ? kGaveUp : wtop);
+      }
+      ptx::cluster_barrier();
+    } else {
+      if (lane == 0) {
+        sh.sum[par][warp] = ss;
+        sh.top[par][warp] = wtop;
+      }
+      quit = __syncthreads_or(!ok) != 0;  // the whole CTA agrees on giving up
+      if (quit) break;
+      if (tid == 0 && next < p.rows) issue();
     }
-    if (__syncthreads_or(!ok)) break;  // the whole CTA agrees on giving up
-    if (tid == 0 && next < p.rows) issue();
-    ss = join_sum(sh.sum[par], warps);
-    const uint32_t tbits = join_max(sh.top[par], warps);
+    ss = join_sum<CL>(sh.sum[par], slots);
+    const uint32_t tbits = join_max<CL>(sh.top[par], slots);
+    if (CL) {
+      quit = tbits == kGaveUp;  // so does the cluster
+      if (quit) break;
+      if (tid == 0 && next < p.rows) issue();
+    }
     const float rstd = rsqrtf(fmaf(ss, inv_cols, p.eps));
     float amax = __fmul_rn(__uint_as_float(tbits), rstd);
     const bool special = tbits >= kInfBits || !(amax <= FLT_MAX);
@@ -452,16 +490,23 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
         fin = fmaxf(fin, vt);
       }
       const uint32_t wfin = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fin));
-      __syncthreads();  // everyone has read this row's maxima
-      if (lane == 0) sh.top[par][warp] = wfin;
-      __syncthreads();
-      amax = __uint_as_float(join_max(sh.top[par], warps));
+      // everyone has read this row's maxima, then they are the finite ones
+      if (CL) {
+        ptx::cluster_barrier();
+        if (lane < ctas) ptx::store_cluster(&sh.top[par][rank * warps + warp], lane, wfin);
+        ptx::cluster_barrier();
+      } else {
+        __syncthreads();
+        if (lane == 0) sh.top[par][warp] = wfin;
+        __syncthreads();
+      }
+      amax = __uint_as_float(join_max<CL>(sh.top[par], slots));
     }
-    if (tid == 0 && p.rstd_out) p.rstd_out[row] = rstd;
+    if (tid == 0 && rank == 0 && p.rstd_out) p.rstd_out[row] = rstd;
     float m[ITEMS];
     if (group == 0) {
       m[0] = multiplier_of(amax, p.fmt);
-      if (tid == 0) p.scales[row] = __fdiv_rn(1.0f, m[0]);
+      if (tid == 0 && rank == 0) p.scales[row] = __fdiv_rn(1.0f, m[0]);
 #pragma unroll
       for (int it = 1; it < ITEMS; ++it) m[it] = m[0];
     } else {
@@ -469,7 +514,7 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
 #pragma unroll
         for (int it = 0; it < ITEMS; ++it) vtop[it] = fmaxf(vtop[it], __shfl_xor_sync(0xFFFFFFFFu, vtop[it], o));
       }
-      float* srow = p.scales + static_cast<int64_t>(row) * p.nb;
+      float* srow = p.scales + static_cast<int64_t>(row) * p.nb + (CL ? rank * (share >> group_log) : 0);
       const int in = lane & (group - 1);
       if (group >= ITEMS) {  // lane `in` of a group divides for the group's block of item `in`
         float mine = vtop[0];
@@ -494,7 +539,7 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
     for (int it = 0; it < ITEMS; ++it) {
       const int v = it * T + tid;
       if (v < nv) {
-        const int c0 = v * VEC - shift;
+        const int c0 = col0 + v * VEC;
         const int64_t at = row_at + c0;
         const float2* y = h + it * (VEC / 2);
         uint32_t c4[VEC / 4];
@@ -515,7 +560,7 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1) k_rmsnorm_ring(c
     if (++stage == stages) { stage = 0; phase ^= 1u; }
     par ^= 1;
   }
-  if (sh.abort_flag) {
+  if (quit) {
     if (tid == 0) drain_stages(sh.full, stages, stage, phase, next_stage);
     __syncthreads();
   }
@@ -587,28 +632,34 @@ __device__ __forceinline__ bool team_any(int team, int T, bool say) {
 // `teams` teams of T threads with a row and a ring each (narrow rows: enough
 // rows in flight without a partial row of dw per row).  Both passes over a
 // row (the mean, then dx and dw) read its stage, so the stage of row i is
-// refilled after row i + 1's barrier.  dw stays in registers; the teams'
+// refilled after row i + 1's barrier (two stages at least, or one row).  dw stays in registers; the teams'
 // sums join in order through shared memory.
-template <int XT, int E, bool DRES, bool WIDE, bool SHIFT>
-__global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
+template <int XT, int E, bool DRES, bool SHIFT, bool CL>
+__global__ void __launch_bounds__(ring_max_threads(E), 1)
     k_rmsnorm_bwd_ring(const NormBwdParams p, const int teams, const int stages, unsigned* err) {
   constexpr int VEC = vec_elems<XT>();
   constexpr int ITEMS = E / VEC;
-  constexpr bool kWeightRegs = !WIDE;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kTeams][kRingStages];
-  __shared__ float sums[2][32];  // by row parity, per warp of the CTA
+  __shared__ float sums[2][kRingSlots];  // by row parity, per warp of the CTA (or cluster)
+  __shared__ uint32_t gave_up[2][kRingSlots];  // CL: which of them gave up a wait
   __shared__ int abort_flag;
   const int T = blockDim.x / teams;
   const int team = threadIdx.x / T, tid = threadIdx.x - team * T;
   const int lane = tid & 31, warps = T >> 5;
   // rows of this team: first, first + stride, .. (grid and teams are small: all in int)
-  const int first = static_cast<int>(blockIdx.x) * teams + team;
-  const int stride = static_cast<int>(gridDim.x) * teams;
+  const int ctas = CL ? static_cast<int>(ptx::cluster_size()) : 1, rank = CL ? static_cast<int>(ptx::cluster_rank()) : 0;
+  const int unit = CL ? static_cast<int>(blockIdx.x) / ctas : static_cast<int>(blockIdx.x);
+  const int first = unit * teams + team;
+  const int stride = (CL ? static_cast<int>(gridDim.x) / ctas : static_cast<int>(gridDim.x)) * teams;
   // columns before the row in its first vector; the same for all rows of a team
   const int shift = SHIFT ? static_cast<int>(static_cast<int64_t>(first) * p.cols % VEC) : 0;
-  const int nv = (shift + p.cols + VEC - 1) / VEC;
-  const uint32_t row_bytes = SHIFT ? shifted_vecs<VEC>(p.cols) * 16u : static_cast<uint32_t>(nv) * 16u;  // room in a stage
+  const int all = (shift + p.cols + VEC - 1) / VEC;
+  const int share = CL ? cluster_share<VEC, SHIFT>(p.cols, ctas) : all;  // vectors per CTA
+  const int nv = CL ? max(0, min(share, all - rank * share)) : all;
+  const int col0 = (CL ? rank * share * VEC : 0) - shift;  // this CTA's first column
+  // room in a stage
+  const uint32_t row_bytes = CL ? share * 16u : SHIFT ? shifted_vecs<VEC>(p.cols) * 16u : static_cast<uint32_t>(nv) * 16u;
   const uint32_t stage_bytes = row_bytes * (DRES ? 3 : 2);
   const int64_t total = static_cast<int64_t>(p.rows) * p.cols;
   uint8_t* ring = smem + team * stages * stage_bytes;
@@ -618,13 +669,14 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
     ptx::fence_mbarrier_init();
   }
   __syncthreads();
+  if (CL) ptx::cluster_barrier();  // all CTAs of the cluster are there to be written to
   pdl_wait();
   pdl_launch_dependents();
   int next = first;  // thread 0: the next row to bring in, and its stage
   int next_stage = 0;
   auto issue = [&] {
     const int s = next_stage;
-    const int64_t at = static_cast<int64_t>(next) * p.cols - shift;  // a multiple of VEC
+    const int64_t at = static_cast<int64_t>(next) * p.cols + col0;  // a multiple of VEC
     const int64_t off = at * elem_bytes<XT>();
     // whole vectors inside the tensor
     const uint32_t bytes = (SHIFT && at + static_cast<int64_t>(nv) * VEC > total ? nv - 1 : nv) * 16u;
@@ -640,14 +692,14 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
   if (tid == 0)
     for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
-  float2 w[kWeightRegs ? E / 2 : 1], dw[E / 2];
+  float2 w[E / 2], dw[E / 2];
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
     const int v = it * T + tid;
-    if (kWeightRegs && v < nv) {
-      float* wv = reinterpret_cast<float*>(w + (kWeightRegs ? it * (VEC / 2) : 0));
-      if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, v * VEC - shift, p.cols, wv);
-      else load_weight<VEC>(p.weight, p.wt, v * VEC, wv);
+    if (v < nv) {
+      float* wv = reinterpret_cast<float*>(w + it * (VEC / 2));
+      if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, col0 + v * VEC, p.cols, wv);
+      else load_weight<VEC>(p.weight, p.wt, col0 + v * VEC, wv);
     }
 #pragma unroll
     for (int j = 0; j < VEC / 2; ++j) dw[it * (VEC / 2) + j] = make_float2(0.0f, 0.0f);
@@ -656,6 +708,7 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
   int stage = 0;
   uint32_t phase = 0;
   bool ahead = false;  // a row of this team is done
+  bool quit = false;
   int par = 0;
   for (int row = first; row < p.rows;) {
     const float rs = rs_next;
@@ -666,9 +719,9 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
     const uint4* hs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
     const uint4* ds = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 2 * row_bytes);
     const int64_t row_at = static_cast<int64_t>(row) * p.cols;
-    const bool cut = SHIFT && row_at - shift + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
+    const bool cut = SHIFT && row_at + col0 + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
     auto fetch = [&](const uint4* stage_row, const void* src, int v, float2* f) {
-      const int c0 = v * VEC - shift;
+      const int c0 = col0 + v * VEC;
       if (SHIFT && is_edge<VEC>(c0, p.cols))
         widen_edge<XT, VEC>(stage_row[v], src, row_at, c0, p.cols, cut && v == nv - 1, reinterpret_cast<float*>(f));
       else
@@ -680,72 +733,77 @@ __global__ void __launch_bounds__(ring_max_threads(E, WIDE), 1)
     for (int it = 0; it < ITEMS; ++it) {
       const int v = it * T + tid;
       if (v < nv) {
-        float2 g[VEC / 2], h[VEC / 2], wl[VEC / 2];
+        float2 g[VEC / 2], h[VEC / 2];
         fetch(gs, p.dy, v, g);
         fetch(hs, p.h, v, h);
-        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
 #pragma unroll
-        for (int j = 0; j < VEC / 2; ++j)
-          dot2 = f2_fma(f2_mul(g[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]), h[j], dot2);
+        for (int j = 0; j < VEC / 2; ++j) dot2 = f2_fma(f2_mul(g[j], w[it * (VEC / 2) + j]), h[j], dot2);
       }
     }
     float dot = warp_sum(dot2.x + dot2.y);
-    if (lane == 0) sums[par][threadIdx.x >> 5] = dot;
-    if (team_any(team, T, !ok)) break;  // the team agrees on giving up
+    if (CL) {
+      const bool out_of_time = __any_sync(0xFFFFFFFFu, !ok);
+      if (lane < ctas) {
+        const int slot = rank * warps + static_cast<int>(threadIdx.x >> 5);
+        ptx::store_cluster(&sums[par][slot], lane, __float_as_uint(dot));
+        ptx::store_cluster(&gave_up[par][slot], lane, out_of_time ? kGaveUp : 0u);
+      }
+      ptx::cluster_barrier();
+      quit = join_max<true>(gave_up[par], warps * ctas) == kGaveUp;  // the cluster agrees on giving up
+    } else {
+      if (lane == 0) sums[par][threadIdx.x >> 5] = dot;
+      quit = team_any(team, T, !ok);  // so does the team
+    }
+    if (quit) break;
     // behind this barrier nobody reads the previous row's stage any more
-    if (tid == 0 && ahead && stages > 1 && next < p.rows) issue();
+    if (tid == 0 && ahead && next < p.rows) issue();
     ahead = true;
-    if (warps > 1) dot = join_sum(sums[par] + team * warps, warps);
+    if (CL) dot = join_sum<true>(sums[par], warps * ctas);
+    else if (warps > 1) dot = join_sum<false>(sums[par] + team * warps, warps);
     const float mean = -rs * (dot * inv_cols);
     const float2 mean2 = make_float2(mean, mean);  // -mean(gw xh)
 #pragma unroll
     for (int it = 0; it < ITEMS; ++it) {
       const int v = it * T + tid;
       if (v < nv) {
-        float2 g[VEC / 2], h[VEC / 2], d[VEC / 2], wl[VEC / 2];
+        float2 g[VEC / 2], h[VEC / 2], d[VEC / 2];
         fetch(gs, p.dy, v, g);
         fetch(hs, p.h, v, h);
         if (DRES) fetch(ds, p.dres, v, d);
-        if (!kWeightRegs) load_weight<VEC>(p.weight, p.wt, v * VEC, reinterpret_cast<float*>(wl));
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
           const float2 xh = f2_mul(h[j], rs2);
-          const float2 gw = f2_mul(g[j], kWeightRegs ? w[kWeightRegs ? it * (VEC / 2) + j : 0] : wl[j]);
+          const float2 gw = f2_mul(g[j], w[it * (VEC / 2) + j]);
           dw[it * (VEC / 2) + j] = f2_fma(g[j], xh, dw[it * (VEC / 2) + j]);
           const float2 t = f2_fma(xh, mean2, gw);
           d[j] = DRES ? f2_fma(t, rs2, d[j]) : f2_mul(t, rs2);
         }
-        const int c0 = v * VEC - shift;
+        const int c0 = col0 + v * VEC;
         if (SHIFT && is_edge<VEC>(c0, p.cols))
           store_edge<XT, VEC>(p.dx, row_at, c0, p.cols, reinterpret_cast<const float*>(d));
         else
           vec_store(static_cast<char*>(p.dx) + (row_at + c0) * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(d)));
       }
     }
-    if (stages == 1) {  // one row fits: it is refilled once both passes are through
-      team_any(team, T, false);
-      if (tid == 0 && next < p.rows) issue();
-    }
     if (++stage == stages) { stage = 0; phase ^= 1u; }
     par ^= 1;
     row = row_next;
   }
-  if (abort_flag && tid == 0) drain_stages(full[team], stages, stage, phase, next_stage);
-  if (p.part == nullptr && abort_flag == 0) return;
-  __syncthreads();  // every team is through with its ring
-  if (abort_flag) return;
-  float* to = teams == 1 ? p.part + static_cast<int64_t>(blockIdx.x) * p.cols
+  if (quit && tid == 0) drain_stages(full[team], stages, stage, phase, next_stage);
+  if (p.part == nullptr && !quit) return;
+  if (__syncthreads_or(quit)) return;  // every team is through with its ring
+  float* to = teams == 1 ? p.part + static_cast<int64_t>(unit) * p.cols
                          : reinterpret_cast<float*>(smem) + static_cast<int64_t>(team) * p.cols;
 #pragma unroll
   for (int it = 0; it < ITEMS; ++it) {
     const int v = it * T + tid;
     if (SHIFT) {
-      if (v < nv) store_edge<0, VEC>(to, 0, v * VEC - shift, p.cols, reinterpret_cast<const float*>(dw + it * (VEC / 2)));
+      if (v < nv) store_edge<0, VEC>(to, 0, col0 + v * VEC, p.cols, reinterpret_cast<const float*>(dw + it * (VEC / 2)));
     } else if (v < nv) {
 #pragma unroll
       for (int j = 0; j < VEC / 2; j += 2) {
         const float2 a = dw[it * (VEC / 2) + j], b = dw[it * (VEC / 2) + j + 1];
-        *reinterpret_cast<float4*>(to + v * VEC + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
+        *reinterpret_cast<float4*>(to + col0 + v * VEC + 2 * j) = make_float4(a.x, a.y, b.x, b.y);
       }
     }
   }
@@ -828,8 +886,8 @@ int ring_share(int64_t cols) {
   double busy = 0.0;
   for (int e : {16, 24, 32}) {
     const int t = ring_threads(cols, e);
-    if (t > ring_max_threads(e, false) || (e == 32 && best != 0)) continue;
-    const double b = static_cast<double>(ring_max_threads(e, false) / t) * static_cast<double>(cols) / e;
+    if (t > ring_max_threads(e) || (e == 32 && best != 0)) continue;
+    const double b = static_cast<double>(ring_max_threads(e) / t) * static_cast<double>(cols) / e;
     if (b > busy) { busy = b; best = e; }
   }
   return best;
@@ -845,33 +903,119 @@ int64_t reach(int64_t cols) {
   return SHIFT ? shifted_vecs<vec_elems<XT>()>(static_cast<int>(cols)) * vec_elems<XT>() : cols;
 }
 
-template <int XT, int E, bool RES, bool SHIFT, bool WIDE = false>
+// Shared memory of a CTA beside its stages.
+constexpr int kNormSpare = 1024 + 1024, kBwdSpare = 2048 + 1024;
+// Whether a row is more than a CTA's columns or two stages take.
+template <int XT, bool SHIFT>
+bool wide(int64_t cols, int tensors) {
+  return reach<XT, SHIFT>(cols) > kRingMaxCols || 2 * stage_row<XT, SHIFT>(cols) * tensors > kRingSmem - kBwdSpare;
+}
+// A row has two whole vectors at least, wherever it starts.
+template <int XT>
+bool shift_fits(int64_t cols) {
+  return cols >= 3 * vec_elems<XT>();
+}
+
+template <int XT, int E, bool RES, bool SHIFT>
 cudaError_t norm_ring(const NormArgs& a, const NormParams& p) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = open_smem(k_rmsnorm_ring<XT, E, RES, WIDE, SHIFT>, done);
+  const cudaError_t e = open_smem(k_rmsnorm_ring<XT, E, RES, SHIFT, false>, done);
   if (e != cudaSuccess) return e;
   const int64_t stage = stage_row<XT, SHIFT>(a.cols) * (RES ? 2 : 1);
   const int threads = ring_threads(reach<XT, SHIFT>(a.cols), E);
   // as many CTAs on an SM as the registers allow, while two stages each fit
-  int ctas = ring_max_threads(E, WIDE) / threads;
+  int ctas = ring_max_threads(E) / threads;
   if (ctas > 32) ctas = 32;
-  while (ctas > 1 && (kRingSmem / ctas - 1024) / stage < 2) --ctas;
-  int64_t stages = (kRingSmem / ctas - 1024) / stage;
+  while (ctas > 1 && (kRingSmem / ctas - kNormSpare) / stage < 2) --ctas;
+  int64_t stages = (kRingSmem / ctas - kNormSpare) / stage;
   if (stages > kRingStages) stages = kRingStages;
   const int64_t most = static_cast<int64_t>(sm_count()) * ctas;
   // a CTA's rows start at one place of a vector: VEC rows apart, or one row
   const int64_t grid = a.rows <= most ? a.rows : SHIFT ? most / vec_elems<XT>() * vec_elems<XT>() : most;
   const int64_t per = (a.rows + grid - 1) / grid;
   if (stages > per) stages = per;
-  return launch_pdl(k_rmsnorm_ring<XT, E, RES, WIDE, SHIFT>, dim3(static_cast<unsigned>(grid)), dim3(threads),
+  return launch_pdl(k_rmsnorm_ring<XT, E, RES, SHIFT, false>, dim3(static_cast<unsigned>(grid)), dim3(threads),
                     static_cast<size_t>(stages * stage), a.stream, false, p, static_cast<int>(stages), device_error_word());
+}
+
+// How rows are split over a cluster: its CTAs (the fewest whose share leaves
+// room for two stages and keeps to 512 threads of 24 elements; 4 take the
+// widest rows of f32 with three tensors), elements per thread and stages.
+// A CTA's share is wide enough that one runs on an SM.  tensors: rows that a
+// stage holds; spare: shared memory of a CTA beside its stages.
+struct ClusterPlan {
+  int ctas, e, threads, stages;
+  size_t smem;
+};
+template <int XT, bool SHIFT>
+ClusterPlan cluster_plan(int64_t cols, int tensors, int spare) {
+  ClusterPlan c{};
+  for (c.ctas = 2;; c.ctas *= 2) {
+    const int share = cluster_share<vec_elems<XT>(), SHIFT>(static_cast<int>(cols), c.ctas);
+    const int64_t stage = static_cast<int64_t>(share) * 16 * tensors;
+    c.e = share * vec_elems<XT>() <= 16 * 512 ? 16 : 24;
+    c.threads = ring_threads(static_cast<int64_t>(share) * vec_elems<XT>(), c.e);
+    if (c.ctas < 4 && (c.threads > 512 || 2 * stage > kRingSmem - spare)) continue;
+    c.stages = static_cast<int>((kRingSmem - spare) / stage);
+    if (c.stages > kRingStages) c.stages = kRingStages;
+    c.smem = static_cast<size_t>(c.stages * stage);
+    return c;
+  }
+}
+
+// The clusters of a plan that run at the same time; the last answer is kept
+// (the same on every B200).
+template <typename K>
+int clusters_at_once(K kernel, const ClusterPlan& c, std::atomic<uint64_t>& last) {
+  const uint64_t key = (static_cast<uint64_t>(c.smem) << 32) | (static_cast<uint64_t>(c.threads) << 20) | (c.ctas << 16);
+  const uint64_t known = last.load(std::memory_order_acquire);
+  if ((known & ~0xFFFFull) == key && (known & 0xFFFF) != 0) return static_cast<int>(known & 0xFFFF);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(c.ctas * 16, 1, 1);
+  cfg.blockDim = dim3(c.threads, 1, 1);
+  cfg.dynamicSmemBytes = c.smem;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = c.ctas;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  int fit = 0;
+  if (cudaOccupancyMaxActiveClusters(&fit, kernel, &cfg) != cudaSuccess || fit < 1) {
+    cudaGetLastError();
+    fit = sm_count() / c.ctas;
+  }
+  last.store(key | static_cast<uint64_t>(fit), std::memory_order_release);
+  return fit;
+}
+
+// the clusters to launch: a row each, or as many as run at the same time
+template <int XT, bool SHIFT>
+int64_t cluster_grid(int64_t rows, int64_t most) {
+  constexpr int64_t kVec = vec_elems<XT>();
+  if (rows <= most) return rows;
+  return SHIFT && most >= kVec ? most / kVec * kVec : SHIFT ? kVec : most;
+}
+
+template <int XT, int E, bool RES, bool SHIFT>
+cudaError_t norm_cluster(const NormArgs& a, const NormParams& p, const ClusterPlan& c) {
+  static std::atomic<uint64_t> done{0}, last{0};
+  const auto kernel = k_rmsnorm_ring<XT, E, RES, SHIFT, true>;
+  const cudaError_t e = open_smem(kernel, done);
+  if (e != cudaSuccess) return e;
+  const int64_t grid = cluster_grid<XT, SHIFT>(a.rows, clusters_at_once(kernel, c, last));
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid * c.ctas)), dim3(c.threads), c.smem, a.stream, c.ctas, p,
+                            c.stages, device_error_word());
 }
 
 template <int XT, bool RES, bool SHIFT>
 cudaError_t norm_ring_any(const NormArgs& a, const NormParams& p) {
   const int64_t cols = reach<XT, SHIFT>(a.cols);
-  if constexpr (!SHIFT)
-    if (cols > kRingMaxCols) return norm_ring<XT, 32, RES, SHIFT, true>(a, p);
+  if (wide<XT, SHIFT>(a.cols, RES ? 2 : 1)) {
+    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.cols, RES ? 2 : 1, kNormSpare);
+    return c.e == 16 ? norm_cluster<XT, 16, RES, SHIFT>(a, p, c) : norm_cluster<XT, 24, RES, SHIFT>(a, p, c);
+  }
   if (a.rows <= sm_count() && cols <= 8 * 1024) return norm_ring<XT, 8, RES, SHIFT>(a, p);
   switch (ring_share(cols)) {
     case 32: return norm_ring<XT, 32, RES, SHIFT>(a, p);
@@ -881,24 +1025,16 @@ cudaError_t norm_ring_any(const NormArgs& a, const NormParams& p) {
   }
 }
 
-// Rows that start between 16-byte boundaries take the ring where their
-// vectors lie in its reach and a row has two whole ones at least.
-template <int XT>
-bool shift_fits(int64_t cols, int64_t tensors, int64_t smem) {
-  return cols >= 3 * vec_elems<XT>() && reach<XT, true>(cols) <= kRingMaxCols && stage_row<XT, true>(cols) * tensors <= smem;
-}
-
 template <int XT>
 cudaError_t norm_run(const NormArgs& a, const NormParams& p) {
   constexpr int VEC = vec_elems<XT>();
   const int group = p.block / VEC;
-  const int64_t tensors = a.residual ? 2 : 1;
   const bool vecs = aligned16(a.x) && aligned16(a.residual) && aligned16(a.residual_out) && aligned16(a.y_out) &&
                     reinterpret_cast<uintptr_t>(a.q) % VEC == 0 &&
                     (p.block == 0 || (group <= 32 && (group & (group - 1)) == 0));
-  if (vecs && a.cols % VEC == 0 && aligned16(a.weight) && a.cols * elem_bytes<XT>() * tensors <= kRingSmem - 1024)
+  if (vecs && a.cols % VEC == 0 && aligned16(a.weight))
     return a.residual ? norm_ring_any<XT, true, false>(a, p) : norm_ring_any<XT, false, false>(a, p);
-  if (vecs && p.block == 0 && shift_fits<XT>(a.cols, tensors, kRingSmem - 1024))
+  if (vecs && p.block == 0 && shift_fits<XT>(a.cols))
     return a.residual ? norm_ring_any<XT, true, true>(a, p) : norm_ring_any<XT, false, true>(a, p);
   const int64_t grid = a.rows < 8 * sm_count() ? a.rows : 8 * sm_count();
   return launch_pdl(k_rmsnorm_any<XT>, dim3(static_cast<unsigned>(grid)), dim3(kAnyThreads), 0, a.stream, false, p);
@@ -906,32 +1042,43 @@ cudaError_t norm_run(const NormArgs& a, const NormParams& p) {
 
 int64_t bwd_parts(int64_t rows) { return rows < kBwdParts ? rows : kBwdParts; }
 
-template <int XT, int E, bool DRES, bool SHIFT, bool WIDE = false>
+template <int XT, int E, bool DRES, bool SHIFT>
+cudaError_t bwd_cluster(const NormBwdArgs& a, const NormBwdParams& p, const ClusterPlan& c, int64_t& grid) {
+  static std::atomic<uint64_t> done{0}, last{0};
+  const auto kernel = k_rmsnorm_bwd_ring<XT, E, DRES, SHIFT, true>;
+  const cudaError_t e = open_smem(kernel, done);
+  if (e != cudaSuccess) return e;
+  grid = cluster_grid<XT, SHIFT>(a.rows, clusters_at_once(kernel, c, last));  // partial rows too
+  return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid * c.ctas)), dim3(c.threads), c.smem, a.stream, c.ctas, p, 1,
+                            c.stages, device_error_word());
+}
+
+template <int XT, int E, bool DRES, bool SHIFT>
 cudaError_t bwd_ring(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
   static std::atomic<uint64_t> done{0};
-  const cudaError_t e = open_smem(k_rmsnorm_bwd_ring<XT, E, DRES, WIDE, SHIFT>, done);
+  const cudaError_t e = open_smem(k_rmsnorm_bwd_ring<XT, E, DRES, SHIFT, false>, done);
   if (e != cudaSuccess) return e;
   const int64_t stage = stage_row<XT, SHIFT>(a.cols) * (DRES ? 3 : 2);
   const int T = ring_threads(reach<XT, SHIFT>(a.cols), E);
-  const int half = ring_max_threads(E, WIDE) / 2;
+  const int half = ring_max_threads(E) / 2;
   // CTAs of half the threads that the registers allow, two to an SM, while
   // every team has a row
   int teams = half / T;
   if (teams > kTeams) teams = kTeams;
   const int64_t sms = sm_count();
-  while (teams > 1 && (static_cast<int64_t>(teams) * sms >= 2 * a.rows || 2 * teams * stage > kRingSmem / 2 - 2048)) --teams;
+  while (teams > 1 && (static_cast<int64_t>(teams) * sms >= 2 * a.rows || 2 * teams * stage > kRingSmem / 2 - kBwdSpare)) --teams;
   if (teams < 1) teams = 1;
-  const int ctas = (T * teams <= half && 2 * teams * stage <= kRingSmem / 2 - 2048) ? 2 : 1;
+  const int ctas = (T * teams <= half && 2 * teams * stage <= kRingSmem / 2 - kBwdSpare) ? 2 : 1;
   int64_t most = sms * ctas;
   if (most > kBwdParts) most = kBwdParts;
   grid = (a.rows + teams - 1) / teams;
   // a team's rows start at one place of a vector: VEC rows apart, or one row
   if (grid > most) grid = SHIFT ? most / vec_elems<XT>() * vec_elems<XT>() : most;
   const int64_t per = (a.rows + grid * teams - 1) / (grid * teams);
-  int64_t stages = (kRingSmem / ctas - 2048) / (teams * stage);
+  int64_t stages = (kRingSmem / ctas - kBwdSpare) / (teams * stage);
   if (stages > kRingStages) stages = kRingStages;
   if (stages > per) stages = per;
-  return launch_pdl(k_rmsnorm_bwd_ring<XT, E, DRES, WIDE, SHIFT>, dim3(static_cast<unsigned>(grid)), dim3(T * teams),
+  return launch_pdl(k_rmsnorm_bwd_ring<XT, E, DRES, SHIFT, false>, dim3(static_cast<unsigned>(grid)), dim3(T * teams),
                     static_cast<size_t>(stages * teams * stage), a.stream, false, p, teams, static_cast<int>(stages),
                     device_error_word());
 }
@@ -939,8 +1086,10 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid
 template <int XT, bool DRES, bool SHIFT>
 cudaError_t bwd_ring_any(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
   const int64_t cols = reach<XT, SHIFT>(a.cols);
-  if constexpr (!SHIFT)
-    if (cols > kRingMaxCols) return bwd_ring<XT, 32, DRES, SHIFT, true>(a, p, grid);
+  if (wide<XT, SHIFT>(a.cols, DRES ? 3 : 2)) {
+    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.cols, DRES ? 3 : 2, kBwdSpare);
+    return c.e == 16 ? bwd_cluster<XT, 16, DRES, SHIFT>(a, p, c, grid) : bwd_cluster<XT, 24, DRES, SHIFT>(a, p, c, grid);
+  }
   switch (ring_share(cols)) {
     case 32: return bwd_ring<XT, 32, DRES, SHIFT>(a, p, grid);
     case 24: return bwd_ring<XT, 24, DRES, SHIFT>(a, p, grid);
@@ -953,11 +1102,10 @@ cudaError_t bwd_ring_any(const NormBwdArgs& a, const NormBwdParams& p, int64_t& 
 template <int XT>
 cudaError_t bwd_run(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
   constexpr int VEC = vec_elems<XT>();
-  const int64_t tensors = a.dres ? 3 : 2;
   const bool vecs = aligned16(a.dy) && aligned16(a.h) && aligned16(a.dres) && aligned16(a.dx);
-  if (vecs && a.cols % VEC == 0 && aligned16(a.weight) && a.cols * elem_bytes<XT>() * tensors <= kRingSmem - 2048)
+  if (vecs && a.cols % VEC == 0 && aligned16(a.weight))
     return a.dres ? bwd_ring_any<XT, true, false>(a, p, grid) : bwd_ring_any<XT, false, false>(a, p, grid);
-  if (vecs && shift_fits<XT>(a.cols, tensors, kRingSmem - 2048))
+  if (vecs && shift_fits<XT>(a.cols))
     return a.dres ? bwd_ring_any<XT, true, true>(a, p, grid) : bwd_ring_any<XT, false, true>(a, p, grid);
   const size_t smem = p.part ? static_cast<size_t>(a.cols) * 4 : 0;
   if (smem > 48 * 1024) {

@@ -381,3 +381,60 @@ def test_neighbouring_rows_do_not_mix(cols, dtype):
     for a, b in ((q, q2), (s, s2), (h, h2), (dx, dx2)):
         assert torch.equal(a[~bad], b[~bad])
     assert bool((q2[bad] == 0x7F).all()) and bool(torch.isnan(dx2[bad]).all())
+
+
+# ------------------------------------------- rows split over a cluster's CTAs
+WIDE = [(torch.bfloat16, 20480), (torch.bfloat16, 28672), (torch.float16, 16401), (torch.float32, 9600),
+        (torch.float32, 18944), (torch.float32, 28672), (torch.float32, 32765)]
+
+
+@pytest.mark.parametrize("dtype,cols", WIDE)
+@pytest.mark.parametrize("rows", [1, 301])
+def test_wide_rows(rows, dtype, cols):
+    wdtype = torch.float32 if rows == 1 else dtype
+    x, w, r = inputs(rows, cols, dtype, wdtype, True, seed=cols)
+    dy, _, _ = inputs(rows, cols, dtype, wdtype, False, seed=cols + 1)
+    for res, dres in ((r, dy), (None, None)):
+        q, s, h, y, rstd = run_forward(x, w, res, 1e-5, H.E4M3, 0)
+        check_forward(x, w, res, 1e-5, H.E4M3, 0, q, s, h if res is not None else None, y, rstd)
+        dx, dw = H.hq_rmsnorm_backward(r, x, w, rstd, dres=dres)
+        dx2, dw2 = H.hq_rmsnorm_backward(r, x, w, rstd, dres=dres)
+        torch.cuda.synchronize()
+        check_backward(r, x, w, rstd, dres, dx, dw)
+        assert torch.equal(dx, dx2) and torch.equal(dw, dw2)
+    if cols % 16 == 0:
+        for block in (32, 256):
+            q, s, h, y, rstd = run_forward(x, w, r, 1e-5, H.E5M2, block)
+            check_forward(x, w, r, 1e-5, H.E5M2, block, q, s, h, y, rstd)
+
+
+@pytest.mark.parametrize("block", [0, 64])
+def test_infinities_and_nan_in_wide_rows(block):
+    for dtype, cols in ((torch.bfloat16, 28672), (torch.float32, 20480)):
+        x, w, _ = inputs(200, cols, dtype, torch.float32, False, seed=13)
+        clean = run_forward(x, w, None, 1e-5, H.E4M3, block)
+        bad = torch.zeros(200, dtype=torch.bool, device="cuda")
+        for k in range(0, 200, 7):
+            x[k, (k * 997) % cols] = float("nan") if k % 2 else float("inf")
+            bad[k] = True
+        q, s, _, y, rstd = run_forward(x, w, None, 1e-5, H.E4M3, block)
+        yy = x.double() * w.double() * rstd.double()[:, None]
+        assert bool((torch.isnan(y) == torch.isnan(yy)).all())
+        P.check_quantized(q[bad], s[bad], yy[bad], block, H.E4M3, rel_y(cols))
+        for a, b in zip((q, s, y, rstd), (clean[0], clean[1], clean[3], clean[4])):
+            assert torch.equal(a[~bad], b[~bad])
+
+
+def test_wide_rows_on_two_streams_at_once():
+    x, w, r = inputs(150, 28672, torch.bfloat16, torch.bfloat16, True, seed=14)
+    q, s, h = H.hq_rmsnorm_fp8(x, w, 1e-5, residual=r)
+    rstd = torch.rand(150, device="cuda")
+    dx, dw = H.hq_rmsnorm_backward(x, r, w, rstd)
+    torch.cuda.synchronize()
+    side, got = torch.cuda.Stream(), []
+    for _ in range(10):
+        got.append(H.hq_rmsnorm_fp8(x, w, 1e-5, residual=r) + H.hq_rmsnorm_backward(x, r, w, rstd, stream=side))
+    torch.cuda.synchronize()
+    for g in got:
+        assert all(torch.equal(a, b) for a, b in zip(g, (q, s, h, dx, dw)))
+    H.hq_check_device_error()
