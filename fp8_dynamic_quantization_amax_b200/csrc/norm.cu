@@ -82,8 +82,9 @@ struct NormParams {
 // ------------------------------------------------------------ any layout
 // One CTA per row at a time, one element per access, the row read twice (a
 // third time when it holds an infinity or NaN): what the kernels on vectors
-// do not take -- buffers that start off 16-byte boundaries, the narrowest rows
-// and the widest, blocks that are no power of two.
+// do not take -- buffers that start off 16-byte boundaries, rows of less than
+// three vectors between them, blocks that are no power of two of vectors up
+// to 32.
 constexpr int kAnyThreads = 256;
 
 template <int XT>
@@ -179,7 +180,8 @@ constexpr int kRingStages = 8;
 // Rows beyond the columns or the stages of one CTA are split over a cluster
 // (CL): every CTA a run of the row's vectors, the warps' sums and maxima
 // written into all its CTAs' shared memories, a cluster barrier in place of
-// the block's.
+// the block's: [4096, 28672] f32 292 us forward and 427 backward, against 977
+// and 2305 with one element per access.
 constexpr int kRingMaxCols = 16384;
 constexpr int ring_max_threads(int e) { return e == 8 ? 1024 : 512; }
 constexpr int kRingSlots = 64;  // warps of a CTA or cluster
@@ -279,29 +281,54 @@ __device__ __forceinline__ void load_weight(const void* w, int wt, int c, float*
 // the first and last of them shared with the neighbouring rows.  A CTA's (or
 // team's) rows lie a multiple of VEC rows apart, so that they all start at
 // the same place of a vector and the columns that a thread holds, its weights
-// and its sums of dw stay the same: [16384, 1001] bf16 38.9 us forward and
-// 52.9 backward, against 180 and 372 with one element per access.
-// Columns c0 .. c0 + VEC - 1 of such a vector: zero for
-// those of other rows; element by element where the tensor ends inside it.
+// and its sums of dw stay the same: [16384, 1001] bf16 32.6 us forward and
+// 35.6 backward, against 180 and 372 with one element per access.
+// Where the tensor ends inside a row's last vector, the CTA's first thread
+// copies the elements before that end into the stage itself.
+// These helpers keep to few registers: they sit in the kernels' inner loops.
 template <int VEC>
 __device__ __forceinline__ bool is_edge(int c0, int cols) {
   return c0 < 0 || c0 + VEC > cols;
 }
-template <int XT, int VEC>
-__device__ __forceinline__ void widen_edge(const uint4& u, const void* src, int64_t row_at, int c0, int cols, bool cut, float* f) {
-  if (!cut) vec_widen<XT>(u, f);
+// zero in the columns of other rows; the vector starts at column c0
+template <int XT>
+__device__ __forceinline__ void mask_edge(uint4& u, int c0, int cols) {
+  uint32_t* w = reinterpret_cast<uint32_t*>(&u);
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) {
-    const bool in = c0 + j >= 0 && c0 + j < cols;
-    if (!in) f[j] = 0.0f;
-    else if (cut) f[j] = elem_load<XT>(src, row_at + c0 + j);
+  for (int k = 0; k < 4; ++k) {
+    if (XT == 0) {
+      if (static_cast<unsigned>(c0 + k) >= static_cast<unsigned>(cols)) w[k] = 0;
+    } else {
+      if (static_cast<unsigned>(c0 + 2 * k) >= static_cast<unsigned>(cols)) w[k] &= 0xFFFF0000u;
+      if (static_cast<unsigned>(c0 + 2 * k + 1) >= static_cast<unsigned>(cols)) w[k] &= 0x0000FFFFu;
+    }
   }
 }
-template <int XT, int VEC>
-__device__ __forceinline__ void store_edge(void* dst, int64_t row_at, int c0, int cols, const float* f) {
+// the elements of N packed ones of BYTES that are this row's; at: address of column c0
+template <int BYTES, int N>
+__device__ __forceinline__ void store_edge(void* at, int c0, int cols, const uint32_t* w) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j)
-    if (c0 + j >= 0 && c0 + j < cols) elem_store<XT>(dst, row_at + c0 + j, f[j]);
+  for (int j = 0; j < N; ++j) {
+    const uint32_t e = w[j * BYTES / 4] >> (8 * (j * BYTES % 4));
+    if (static_cast<unsigned>(c0 + j) < static_cast<unsigned>(cols)) {
+      if (BYTES == 1) static_cast<uint8_t*>(at)[j] = static_cast<uint8_t>(e);
+      else if (BYTES == 2) static_cast<uint16_t*>(at)[j] = static_cast<uint16_t>(e);
+      else static_cast<uint32_t*>(at)[j] = e;
+    }
+  }
+}
+template <int XT>
+__device__ __forceinline__ void store_edge_vec(void* at, int c0, int cols, const uint4& u) {
+  store_edge<elem_bytes<XT>(), vec_elems<XT>()>(at, c0, cols, reinterpret_cast<const uint32_t*>(&u));
+}
+// the n elements before the tensor's end, into the last vector of a stage's row
+template <int XT>
+__device__ __forceinline__ void copy_tail(void* to, const void* from, int n) {
+#pragma unroll 1
+  for (int j = 0; j < n; ++j) {
+    if (XT == 0) static_cast<float*>(to)[j] = static_cast<const volatile float*>(from)[j];
+    else static_cast<uint16_t*>(to)[j] = static_cast<const volatile uint16_t*>(from)[j];
+  }
 }
 template <int VEC>
 __device__ __forceinline__ void load_weight_edge(const void* w, int wt, int c0, int cols, float* f) {
@@ -361,13 +388,19 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const N
   auto issue = [&] {
     const int s = next_stage;
     const int64_t at = static_cast<int64_t>(next) * p.cols + col0;  // a multiple of VEC
-    // whole vectors inside the tensor
-    const uint32_t bytes = (SHIFT && at + static_cast<int64_t>(nv) * VEC > total ? nv - 1 : nv) * 16u;
+    const char* x = static_cast<const char*>(p.x) + at * elem_bytes<XT>();
+    const char* r = RES ? static_cast<const char*>(p.residual) + at * elem_bytes<XT>() : nullptr;
+    uint8_t* to = ring + s * stage_bytes;
+    uint32_t bytes = nv * 16u;
+    if (SHIFT && at + static_cast<int64_t>(nv) * VEC > total) {
+      bytes -= 16;
+      const int n = static_cast<int>(total - at) - (nv - 1) * VEC;
+      copy_tail<XT>(to + bytes, x + bytes, n);
+      if (RES) copy_tail<XT>(to + row_bytes + bytes, r + bytes, n);
+    }
     ptx::mbar_arrive_expect_tx(&sh.full[s], bytes * (RES ? 2 : 1));
-    ptx::bulk_load(ring + s * stage_bytes, static_cast<const char*>(p.x) + at * elem_bytes<XT>(), bytes, &sh.full[s]);
-    if (RES)
-      ptx::bulk_load(ring + s * stage_bytes + row_bytes, static_cast<const char*>(p.residual) + at * elem_bytes<XT>(), bytes,
-                     &sh.full[s]);
+    ptx::bulk_load(to, x, bytes, &sh.full[s]);
+    if (RES) ptx::bulk_load(to + row_bytes, r, bytes, &sh.full[s]);
     next = p.rows - next > stride ? next + stride : p.rows;  // no overflow near 2^31 rows
     if (++next_stage == stages) next_stage = 0;
   };
@@ -395,7 +428,6 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const N
     const uint4* xs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes);
     const uint4* rs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
     const int64_t row_at = static_cast<int64_t>(row) * p.cols;
-    const bool cut = SHIFT && row_at + col0 + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
     // every vector is asked for before the first is used
     uint4 xr[ITEMS], rr[RES ? ITEMS : 1];
 #pragma unroll
@@ -417,22 +449,21 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const N
       if (v < nv) {
         const int c0 = col0 + v * VEC;
         const bool edge = SHIFT && is_edge<VEC>(c0, p.cols);
-        if (SHIFT && edge) widen_edge<XT, VEC>(xr[it], p.x, row_at, c0, p.cols, cut && v == nv - 1, reinterpret_cast<float*>(hv));
-        else vec_widen<XT>(xr[it], reinterpret_cast<float*>(hv));
+        if (SHIFT && edge) {
+          mask_edge<XT>(xr[it], c0, p.cols);
+          if (RES) mask_edge<XT>(rr[RES ? it : 0], c0, p.cols);
+        }
+        vec_widen<XT>(xr[it], reinterpret_cast<float*>(hv));
         if (RES) {
           float2 r[VEC / 2];
-          if (SHIFT && edge)
-            widen_edge<XT, VEC>(rr[RES ? it : 0], p.residual, row_at, c0, p.cols, cut && v == nv - 1, reinterpret_cast<float*>(r));
-          else
-            vec_widen<XT>(rr[RES ? it : 0], reinterpret_cast<float*>(r));
+          vec_widen<XT>(rr[RES ? it : 0], reinterpret_cast<float*>(r));
 #pragma unroll
           for (int j = 0; j < VEC / 2; ++j) hv[j] = f2_add(hv[j], r[j]);
           if (p.residual_out) {
-            if (SHIFT && edge)
-              store_edge<XT, VEC>(p.residual_out, row_at, c0, p.cols, reinterpret_cast<const float*>(hv));
-            else
-              vec_store(static_cast<char*>(p.residual_out) + (row_at + c0) * elem_bytes<XT>(),
-                        vec_narrow<XT>(reinterpret_cast<const float*>(hv)));
+            const uint4 u = vec_narrow<XT>(reinterpret_cast<const float*>(hv));
+            char* to = static_cast<char*>(p.residual_out) + (row_at + c0) * elem_bytes<XT>();
+            if (SHIFT && edge) store_edge_vec<XT>(to, c0, p.cols, u);
+            else vec_store(to, u);
           }
         }
 #pragma unroll
@@ -544,14 +575,12 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const N
         const float2* y = h + it * (VEC / 2);
         uint32_t c4[VEC / 4];
         codes<VEC>(c4, y, m[it], p.fmt, special);
+        char* yo = static_cast<char*>(p.y_out) + at * elem_bytes<XT>();
         if (SHIFT && is_edge<VEC>(c0, p.cols)) {
-          if (p.y_out) store_edge<XT, VEC>(p.y_out, row_at, c0, p.cols, reinterpret_cast<const float*>(y));
-#pragma unroll
-          for (int j = 0; j < VEC; ++j)
-            if (c0 + j >= 0 && c0 + j < p.cols) p.q[at + j] = static_cast<uint8_t>(c4[j / 4] >> (8 * (j & 3)));
+          if (p.y_out) store_edge_vec<XT>(yo, c0, p.cols, vec_narrow<XT>(reinterpret_cast<const float*>(y)));
+          store_edge<1, VEC>(p.q + at, c0, p.cols, c4);
         } else {
-          if (p.y_out)
-            vec_store(static_cast<char*>(p.y_out) + at * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(y)));
+          if (p.y_out) vec_store(yo, vec_narrow<XT>(reinterpret_cast<const float*>(y)));
           if (VEC == 8) *reinterpret_cast<uint2*>(p.q + at) = make_uint2(c4[0], c4[VEC / 4 - 1]);
           else *reinterpret_cast<uint32_t*>(p.q + at) = c4[0];
         }
@@ -678,10 +707,16 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
     const int s = next_stage;
     const int64_t at = static_cast<int64_t>(next) * p.cols + col0;  // a multiple of VEC
     const int64_t off = at * elem_bytes<XT>();
-    // whole vectors inside the tensor
-    const uint32_t bytes = (SHIFT && at + static_cast<int64_t>(nv) * VEC > total ? nv - 1 : nv) * 16u;
     uint8_t* to = ring + s * stage_bytes;
     uint64_t* bar = &full[team][s];
+    uint32_t bytes = nv * 16u;
+    if (SHIFT && at + static_cast<int64_t>(nv) * VEC > total) {
+      bytes -= 16;
+      const int n = static_cast<int>(total - at) - (nv - 1) * VEC;
+      copy_tail<XT>(to + bytes, static_cast<const char*>(p.dy) + off + bytes, n);
+      copy_tail<XT>(to + row_bytes + bytes, static_cast<const char*>(p.h) + off + bytes, n);
+      if (DRES) copy_tail<XT>(to + 2 * row_bytes + bytes, static_cast<const char*>(p.dres) + off + bytes, n);
+    }
     ptx::mbar_arrive_expect_tx(bar, bytes * (DRES ? 3 : 2));
     ptx::bulk_load(to, static_cast<const char*>(p.dy) + off, bytes, bar);
     ptx::bulk_load(to + row_bytes, static_cast<const char*>(p.h) + off, bytes, bar);
@@ -719,13 +754,10 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
     const uint4* hs = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + row_bytes);
     const uint4* ds = reinterpret_cast<const uint4*>(ring + stage * stage_bytes + 2 * row_bytes);
     const int64_t row_at = static_cast<int64_t>(row) * p.cols;
-    const bool cut = SHIFT && row_at + col0 + static_cast<int64_t>(nv) * VEC > total;  // the last vector leaves the tensor
-    auto fetch = [&](const uint4* stage_row, const void* src, int v, float2* f) {
-      const int c0 = col0 + v * VEC;
-      if (SHIFT && is_edge<VEC>(c0, p.cols))
-        widen_edge<XT, VEC>(stage_row[v], src, row_at, c0, p.cols, cut && v == nv - 1, reinterpret_cast<float*>(f));
-      else
-        vec_widen<XT>(stage_row[v], reinterpret_cast<float*>(f));
+    auto fetch = [&](const uint4* stage_row, int v, float2* f) {
+      uint4 u = stage_row[v];
+      if (SHIFT && is_edge<VEC>(col0 + v * VEC, p.cols)) mask_edge<XT>(u, col0 + v * VEC, p.cols);
+      vec_widen<XT>(u, reinterpret_cast<float*>(f));
     };
     const float2 rs2 = make_float2(rs, rs);
     float2 dot2 = make_float2(0.0f, 0.0f);
@@ -734,8 +766,8 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
       const int v = it * T + tid;
       if (v < nv) {
         float2 g[VEC / 2], h[VEC / 2];
-        fetch(gs, p.dy, v, g);
-        fetch(hs, p.h, v, h);
+        fetch(gs, v, g);
+        fetch(hs, v, h);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) dot2 = f2_fma(f2_mul(g[j], w[it * (VEC / 2) + j]), h[j], dot2);
       }
@@ -767,9 +799,9 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
       const int v = it * T + tid;
       if (v < nv) {
         float2 g[VEC / 2], h[VEC / 2], d[VEC / 2];
-        fetch(gs, p.dy, v, g);
-        fetch(hs, p.h, v, h);
-        if (DRES) fetch(ds, p.dres, v, d);
+        fetch(gs, v, g);
+        fetch(hs, v, h);
+        if (DRES) fetch(ds, v, d);
 #pragma unroll
         for (int j = 0; j < VEC / 2; ++j) {
           const float2 xh = f2_mul(h[j], rs2);
@@ -779,10 +811,10 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
           d[j] = DRES ? f2_fma(t, rs2, d[j]) : f2_mul(t, rs2);
         }
         const int c0 = col0 + v * VEC;
-        if (SHIFT && is_edge<VEC>(c0, p.cols))
-          store_edge<XT, VEC>(p.dx, row_at, c0, p.cols, reinterpret_cast<const float*>(d));
-        else
-          vec_store(static_cast<char*>(p.dx) + (row_at + c0) * elem_bytes<XT>(), vec_narrow<XT>(reinterpret_cast<const float*>(d)));
+        const uint4 u = vec_narrow<XT>(reinterpret_cast<const float*>(d));
+        char* to = static_cast<char*>(p.dx) + (row_at + c0) * elem_bytes<XT>();
+        if (SHIFT && is_edge<VEC>(c0, p.cols)) store_edge_vec<XT>(to, c0, p.cols, u);
+        else vec_store(to, u);
       }
     }
     if (++stage == stages) { stage = 0; phase ^= 1u; }
@@ -798,7 +830,12 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
   for (int it = 0; it < ITEMS; ++it) {
     const int v = it * T + tid;
     if (SHIFT) {
-      if (v < nv) store_edge<0, VEC>(to, 0, col0 + v * VEC, p.cols, reinterpret_cast<const float*>(dw + it * (VEC / 2)));
+      const float* f = reinterpret_cast<const float*>(dw + it * (VEC / 2));
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int c = col0 + v * VEC + j;
+        if (v < nv && c >= 0 && c < p.cols) to[c] = f[j];
+      }
     } else if (v < nv) {
 #pragma unroll
       for (int j = 0; j < VEC / 2; j += 2) {
@@ -938,9 +975,13 @@ cudaError_t norm_ring(const NormArgs& a, const NormParams& p) {
                     static_cast<size_t>(stages * stage), a.stream, false, p, static_cast<int>(stages), device_error_word());
 }
 
-// How rows are split over a cluster: its CTAs (the fewest whose share leaves
-// room for two stages and keeps to 512 threads of 24 elements; 4 take the
-// widest rows of f32 with three tensors), elements per thread and stages.
+// How rows are split over a cluster: its CTAs, elements per thread and stages.
+// Two CTAs where two stages fit and their threads hold no more than max_e
+// elements, four for few rows ([32, 28672] bf16 3.9 us in four, 4.9 in two)
+// and otherwise: the barrier's time counts per row ([4096, 20480] bf16 with a
+// residual 139 us in two, 211 in four, 337 in eight).  max_e is 32, but 16 for
+// the forward pass of f32 rows with a residual, whose vectors take the most
+// registers ([4096, 24576]: 278 us in four CTAs, 326 in two with 24 elements).
 // A CTA's share is wide enough that one runs on an SM.  tensors: rows that a
 // stage holds; spare: shared memory of a CTA beside its stages.
 struct ClusterPlan {
@@ -948,14 +989,15 @@ struct ClusterPlan {
   size_t smem;
 };
 template <int XT, bool SHIFT>
-ClusterPlan cluster_plan(int64_t cols, int tensors, int spare) {
+ClusterPlan cluster_plan(int64_t rows, int64_t cols, int tensors, int spare, int max_e) {
   ClusterPlan c{};
-  for (c.ctas = 2;; c.ctas *= 2) {
+  for (c.ctas = 4 * rows <= sm_count() ? 4 : 2;; c.ctas *= 2) {
     const int share = cluster_share<vec_elems<XT>(), SHIFT>(static_cast<int>(cols), c.ctas);
     const int64_t stage = static_cast<int64_t>(share) * 16 * tensors;
-    c.e = share * vec_elems<XT>() <= 16 * 512 ? 16 : 24;
-    c.threads = ring_threads(static_cast<int64_t>(share) * vec_elems<XT>(), c.e);
-    if (c.ctas < 4 && (c.threads > 512 || 2 * stage > kRingSmem - spare)) continue;
+    const int n = share * vec_elems<XT>();
+    c.e = n <= 16 * 512 ? 16 : n <= 24 * 512 ? 24 : 32;
+    c.threads = ring_threads(n, c.e);
+    if (c.ctas < 4 && (c.threads > 512 || c.e > max_e || 2 * stage > kRingSmem - spare)) continue;
     c.stages = static_cast<int>((kRingSmem - spare) / stage);
     if (c.stages > kRingStages) c.stages = kRingStages;
     c.smem = static_cast<size_t>(c.stages * stage);
@@ -1013,7 +1055,8 @@ template <int XT, bool RES, bool SHIFT>
 cudaError_t norm_ring_any(const NormArgs& a, const NormParams& p) {
   const int64_t cols = reach<XT, SHIFT>(a.cols);
   if (wide<XT, SHIFT>(a.cols, RES ? 2 : 1)) {
-    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.cols, RES ? 2 : 1, kNormSpare);
+    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.rows, a.cols, RES ? 2 : 1, kNormSpare, XT == 0 && RES ? 16 : 32);
+    if (c.e == 32) return norm_cluster<XT, 32, RES, SHIFT>(a, p, c);
     return c.e == 16 ? norm_cluster<XT, 16, RES, SHIFT>(a, p, c) : norm_cluster<XT, 24, RES, SHIFT>(a, p, c);
   }
   if (a.rows <= sm_count() && cols <= 8 * 1024) return norm_ring<XT, 8, RES, SHIFT>(a, p);
@@ -1087,7 +1130,8 @@ template <int XT, bool DRES, bool SHIFT>
 cudaError_t bwd_ring_any(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid) {
   const int64_t cols = reach<XT, SHIFT>(a.cols);
   if (wide<XT, SHIFT>(a.cols, DRES ? 3 : 2)) {
-    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.cols, DRES ? 3 : 2, kBwdSpare);
+    const ClusterPlan c = cluster_plan<XT, SHIFT>(a.rows, a.cols, DRES ? 3 : 2, kBwdSpare, 32);
+    if (c.e == 32) return bwd_cluster<XT, 32, DRES, SHIFT>(a, p, c, grid);
     return c.e == 16 ? bwd_cluster<XT, 16, DRES, SHIFT>(a, p, c, grid) : bwd_cluster<XT, 24, DRES, SHIFT>(a, p, c, grid);
   }
   switch (ring_share(cols)) {
