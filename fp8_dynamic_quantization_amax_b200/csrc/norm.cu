@@ -914,18 +914,21 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) ==
 int ring_threads(int64_t cols, int e) { return static_cast<int>(((cols + e - 1) / e + 31) / 32 * 32); }
 
 // Elements per thread for rows of `cols`: the share that keeps the most of an
-// SM's 512 threads busy, the narrowest of equals (1408 columns of bf16,
-// 47616 rows: 24 elements in 8 CTAs of 64 threads 78 us, 16 elements in 4 of
-// 96 threads 101 us).  32 elements only where 24 do not reach.
-int ring_share(int64_t cols) {
+// SM's 512 threads busy (1408 columns of bf16, 47616 rows: 24 elements in 8
+// CTAs of 64 threads 78 us, 16 elements in 4 of 96 threads 101 us), up to
+// `most` elements unless fewer do not reach.  Of equals the widest for one
+// tensor a row (what a row costs every warp, the joins and divisions, is
+// shared by more elements: [16384, 8192] bf16 without a residual 97 us with
+// 32, 126 with 16), else the narrowest (with one 171 and 145).
+int ring_share(int64_t cols, int most, bool widest) {
   if (cols <= 256) return 8;
   int best = 0;
   double busy = 0.0;
   for (int e : {16, 24, 32}) {
     const int t = ring_threads(cols, e);
-    if (t > ring_max_threads(e) || (e == 32 && best != 0)) continue;
+    if (t > ring_max_threads(e) || (e > most && best != 0)) continue;
     const double b = static_cast<double>(ring_max_threads(e) / t) * static_cast<double>(cols) / e;
-    if (b > busy) { busy = b; best = e; }
+    if (b > busy || (widest && b == busy)) { busy = b; best = e; }
   }
   return best;
 }
@@ -1060,7 +1063,10 @@ cudaError_t norm_ring_any(const NormArgs& a, const NormParams& p) {
     return c.e == 16 ? norm_cluster<XT, 16, RES, SHIFT>(a, p, c) : norm_cluster<XT, 24, RES, SHIFT>(a, p, c);
   }
   if (a.rows <= sm_count() && cols <= 8 * 1024) return norm_ring<XT, 8, RES, SHIFT>(a, p);
-  switch (ring_share(cols)) {
+  // the elements that fit the registers: fewer where rows share vectors, fewer
+  // with a second tensor in f32 (8192 x 5001: 120 us with 16, 186 with 24)
+  constexpr int kMost = !RES && !SHIFT ? 32 : RES && SHIFT && XT == 0 ? 16 : 24;
+  switch (ring_share(cols, kMost, !RES)) {
     case 32: return norm_ring<XT, 32, RES, SHIFT>(a, p);
     case 24: return norm_ring<XT, 24, RES, SHIFT>(a, p);
     case 16: return norm_ring<XT, 16, RES, SHIFT>(a, p);
@@ -1134,7 +1140,7 @@ cudaError_t bwd_ring_any(const NormBwdArgs& a, const NormBwdParams& p, int64_t& 
     if (c.e == 32) return bwd_cluster<XT, 32, DRES, SHIFT>(a, p, c, grid);
     return c.e == 16 ? bwd_cluster<XT, 16, DRES, SHIFT>(a, p, c, grid) : bwd_cluster<XT, 24, DRES, SHIFT>(a, p, c, grid);
   }
-  switch (ring_share(cols)) {
+  switch (ring_share(cols, 24, false)) {
     case 32: return bwd_ring<XT, 32, DRES, SHIFT>(a, p, grid);
     case 24: return bwd_ring<XT, 24, DRES, SHIFT>(a, p, grid);
     case 16: return bwd_ring<XT, 16, DRES, SHIFT>(a, p, grid);
