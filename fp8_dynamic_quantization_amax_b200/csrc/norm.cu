@@ -13,6 +13,11 @@
 // Each CTA adds dw over its rows (in row order) and writes one partial row
 // of f32 sums; a second launch adds the CTAs' partials in CTA order, so the
 // sum has a fixed order and the workspace needs no initial state.
+//
+// Bound: memory where a row brings two tensors or more ([16384, 8192] bf16:
+// 145-159 us with a residual, 6.5-5.9 TB/s; backward 153-163 us, 7.0-6.6
+// TB/s, part of it from L2), instruction issue and the row's serial steps
+// (sum, maximum, divisions) for one tensor a row (97 us, 4.1 TB/s).
 #include "elem.cuh"
 #include "fp8_cvt.cuh"
 #include "hq_internal.cuh"
