@@ -255,39 +255,13 @@ __device__ __forceinline__ uint32_t join_max(const uint32_t* red, int warps) {
   return __reduce_max_sync(0xFFFFFFFFu, v);
 }
 
-// VEC weights from column c as f32 (16-byte aligned weight, c a multiple of VEC)
-template <int VEC>
-__device__ __forceinline__ void load_weight(const void* w, int wt, int c, float* f) {
-  if (wt == 0) {
-#pragma unroll
-    for (int j = 0; j < VEC; j += 4) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c + j));
-      f[j] = v.x; f[j + 1] = v.y; f[j + 2] = v.z; f[j + 3] = v.w;
-    }
-  } else {
-    uint4 u = make_uint4(0, 0, 0, 0);
-    const unsigned short* ws = static_cast<const unsigned short*>(w) + c;
-    if (VEC == 8) {
-      u = __ldg(reinterpret_cast<const uint4*>(ws));
-    } else {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(ws));
-      u.x = v.x; u.y = v.y;
-    }
-    float t[8];
-    if (wt == 1) vec_widen<1>(u, t);
-    else vec_widen<2>(u, t);
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) f[j] = t[j];
-  }
-}
-
 // Rows that start between 16-byte boundaries (SHIFT, a width that is not a
 // whole number of vectors): the row's vectors are those of the whole tensor,
 // the first and last of them shared with the neighbouring rows.  A CTA's (or
 // team's) rows lie a multiple of VEC rows apart, so that they all start at
 // the same place of a vector and the columns that a thread holds, its weights
-// and its sums of dw stay the same: [16384, 1001] bf16 32.6 us forward and
-// 35.6 backward, against 180 and 372 with one element per access.
+// and its sums of dw stay the same: [16384, 1001] bf16 31.2 us forward and
+// 34.0 backward, against 180 and 372 with one element per access.
 // Where the tensor ends inside a row's last vector, the CTA's first thread
 // copies the elements before that end into the stage itself.
 // These helpers keep to few registers: they sit in the kernels' inner loops.
@@ -335,10 +309,52 @@ __device__ __forceinline__ void copy_tail(void* to, const void* from, int n) {
     else static_cast<uint16_t*>(to)[j] = static_cast<const volatile uint16_t*>(from)[j];
   }
 }
-template <int VEC>
-__device__ __forceinline__ void load_weight_edge(const void* w, int wt, int c0, int cols, float* f) {
+// A thread's weights (element type code WT) as f32: vectors tid, tid + T, ...
+// of the nv from column col0.  SHIFT: element by element, zero in other rows'
+// columns.  All loads are in flight together, so nothing about them branches:
+// indices past the row are held at its last (with a branch per element the
+// loads came one after the other, 8 us of a [37, 12307] call's 11).
+template <int WT, int VEC, int ITEMS, bool SHIFT>
+__device__ __forceinline__ void load_weights_as(const void* w, int col0, int cols, int nv, int tid, int T, float* f) {
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) f[j] = (c0 + j >= 0 && c0 + j < cols) ? elem_load_rt(w, wt, c0 + j) : 0.0f;
+  for (int it = 0; it < ITEMS; ++it) {
+    const int c0 = col0 + min(it * T + tid, nv - 1) * VEC;
+    float* o = f + it * VEC;
+    if (SHIFT) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int c = c0 + j;
+        const float e = elem_load_rt(w, WT, max(0, min(c, cols - 1)));
+        o[j] = c >= 0 && c < cols ? e : 0.0f;
+      }
+    } else if (WT == 0) {
+#pragma unroll
+      for (int j = 0; j < VEC; j += 4) {
+        const float4 v = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(w) + c0 + j));
+        o[j] = v.x; o[j + 1] = v.y; o[j + 2] = v.z; o[j + 3] = v.w;
+      }
+    } else {
+      uint4 u = make_uint4(0, 0, 0, 0);
+      const unsigned short* ws = static_cast<const unsigned short*>(w) + c0;
+      if (VEC == 8) {
+        u = __ldg(reinterpret_cast<const uint4*>(ws));
+      } else {
+        const uint2 v = __ldg(reinterpret_cast<const uint2*>(ws));
+        u.x = v.x; u.y = v.y;
+      }
+      float t[8];
+      vec_widen<WT>(u, t);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = t[j];
+    }
+  }
+}
+template <int VEC, int ITEMS, bool SHIFT>
+__device__ __forceinline__ void load_weights(const void* w, int wt, int col0, int cols, int nv, int tid, int T, float2* f) {
+  float* o = reinterpret_cast<float*>(f);
+  if (wt == 0) load_weights_as<0, VEC, ITEMS, SHIFT>(w, col0, cols, nv, tid, T, o);
+  else if (wt == 1) load_weights_as<1, VEC, ITEMS, SHIFT>(w, col0, cols, nv, tid, T, o);
+  else load_weights_as<2, VEC, ITEMS, SHIFT>(w, col0, cols, nv, tid, T, o);
 }
 
 // VEC codes of y * m; EXACT: y may hold NaN
@@ -413,15 +429,7 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1) k_rmsnorm_ring(const N
     for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
   float2 w[E / 2];
-#pragma unroll
-  for (int it = 0; it < ITEMS; ++it) {
-    const int v = it * T + tid;
-    if (v < nv) {
-      float* wv = reinterpret_cast<float*>(w + it * (VEC / 2));
-      if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, col0 + v * VEC, p.cols, wv);
-      else load_weight<VEC>(p.weight, p.wt, col0 + v * VEC, wv);
-    }
-  }
+  load_weights<VEC, ITEMS, SHIFT>(p.weight, p.wt, col0, p.cols, nv, tid, T, w);
   const int group = p.block ? p.block / VEC : 0;  // lanes per block, a power of two
   const int group_log = 31 - __clz(group | 1);
   int stage = 0;
@@ -733,17 +741,9 @@ __global__ void __launch_bounds__(ring_max_threads(E), 1)
     for (int s = 0; s < stages && next < p.rows; ++s) issue();
   const float inv_cols = __fdiv_rn(1.0f, static_cast<float>(p.cols));
   float2 w[E / 2], dw[E / 2];
+  load_weights<VEC, ITEMS, SHIFT>(p.weight, p.wt, col0, p.cols, nv, tid, T, w);
 #pragma unroll
-  for (int it = 0; it < ITEMS; ++it) {
-    const int v = it * T + tid;
-    if (v < nv) {
-      float* wv = reinterpret_cast<float*>(w + it * (VEC / 2));
-      if (SHIFT) load_weight_edge<VEC>(p.weight, p.wt, col0 + v * VEC, p.cols, wv);
-      else load_weight<VEC>(p.weight, p.wt, col0 + v * VEC, wv);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) dw[it * (VEC / 2) + j] = make_float2(0.0f, 0.0f);
-  }
+  for (int j = 0; j < E / 2; ++j) dw[j] = make_float2(0.0f, 0.0f);
   float rs_next = first < p.rows ? __ldg(p.rstd + first) : 0.0f;
   int stage = 0;
   uint32_t phase = 0;
