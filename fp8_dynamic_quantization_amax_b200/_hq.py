@@ -447,6 +447,13 @@ def _like(t, name, shape, dtype):
     return t
 
 
+def _operand(t, name, shape, dtype):
+    """An input of this shape and dtype, its rows made dense where they are not."""
+    if t.shape != shape or t.dtype != dtype:
+        raise ValueError("%s must be %s %s, got %s %s" % (name, tuple(shape), dtype, tuple(t.shape), t.dtype))
+    return t.contiguous()
+
+
 def _out(t, name, shape, dtype, device):
     if t is None:
         return torch.empty(shape, dtype=dtype, device=device)
@@ -475,18 +482,17 @@ def hq_gemm_a8w8_act(xq, wq, x_scale, w_scale, fmt=E4M3, bias=None, act=ACT_NONE
                                     z_q, z_scales)
     if xq.dim() != 2 or wq.dim() != 2 or wq.shape[1] != xq.shape[1]:
         raise ValueError("xq [M, K] and wq [N, K] must be 2-D with one K")
-    xq, wq = xq.contiguous(), wq.contiguous()
     x_scale, w_scale = x_scale.contiguous(), w_scale.contiguous()
     M, K = xq.shape
     N = wq.shape[0]
-    _like(xq, "xq", (M, K), torch.uint8)
-    _like(wq, "wq", (N, K), torch.uint8)
+    xq = _operand(xq, "xq", (M, K), torch.uint8)
+    wq = _operand(wq, "wq", (N, K), torch.uint8)
     if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
         raise ValueError("x_scale and w_scale must be float32")
     if bias is not None:
-        bias = _like(bias.contiguous(), "bias", (N,), torch.bfloat16)
+        bias = _operand(bias, "bias", (N,), torch.bfloat16)
     if residual is not None:
-        residual = _like(residual.contiguous(), "residual", (M, N), torch.bfloat16)
+        residual = _operand(residual, "residual", (M, N), torch.bfloat16)
     out = _out(out, "out", (M, N), torch.bfloat16, xq.device)
     ckpt = ckpt or z_q is not None or z_scales is not None
     if ckpt:
@@ -494,9 +500,9 @@ def hq_gemm_a8w8_act(xq, wq, x_scale, w_scale, fmt=E4M3, bias=None, act=ACT_NONE
             raise ValueError("the checkpoint takes z_block = 32 and N % 32 == 0")
         z_q = _out(z_q, "z_q", (M, N), torch.uint8, xq.device)
         z_scales = _out(z_scales, "z_scales", (M, N // 32), torch.float32, xq.device)
-    check(lib.hq_gemm_a8w8_act(_ptr(xq), _ptr(wq), fmt, _ptr(x_scale), x_scale.numel(), _ptr(w_scale),
-                               w_scale.numel(), _ptr(bias), act, _ptr(residual), M, N, K, _ptr(out), _ptr(z_q), z_fmt,
-                               z_block, _ptr(z_scales), _stream(None)))
+    check(lib.hq_gemm_a8w8_act(xq.data_ptr(), wq.data_ptr(), fmt, x_scale.data_ptr(), x_scale.numel(),
+                               w_scale.data_ptr(), w_scale.numel(), _ptr(bias), act, _ptr(residual), M, N, K,
+                               out.data_ptr(), _ptr(z_q), z_fmt, z_block, _ptr(z_scales), _stream(None)))
     return (out, z_q, z_scales) if ckpt else out
 
 
@@ -518,8 +524,8 @@ def hq_act_backward_fp8(g, z_q, z_scales, act, fmt=E4M3, block=32, dz=None, dbia
     rows, cols = g.shape
     if block <= 0:
         raise ValueError("block must be a positive multiple of 16")
-    z_q = _like(z_q.contiguous(), "z_q", (rows, cols), torch.uint8)
-    z_scales = _like(z_scales.contiguous(), "z_scales", (rows, -(-cols // block)), torch.float32)
+    z_q = _operand(z_q, "z_q", (rows, cols), torch.uint8)
+    z_scales = _operand(z_scales, "z_scales", (rows, -(-cols // block)), torch.float32)
     dz = _out(dz, "dz", (rows, cols), g.dtype, g.device)
     if need_dbias:
         dbias = _out(dbias, "dbias", (cols,), g.dtype, g.device)
@@ -527,8 +533,8 @@ def hq_act_backward_fp8(g, z_q, z_scales, act, fmt=E4M3, block=32, dz=None, dbia
             workspace = torch.empty(hq_act_backward_workspace_bytes(rows, cols), dtype=torch.uint8, device=g.device)
     elif dbias is not None:
         raise ValueError("dbias given with need_dbias=False")
-    check(lib.hq_act_backward_fp8(_ptr(g), _DT[g.dtype], _ptr(z_q), fmt, block, _ptr(z_scales), act, rows, cols,
-                                  _ptr(dz), _ptr(dbias), _ptr(workspace), 0 if workspace is None else
+    check(lib.hq_act_backward_fp8(g.data_ptr(), _DT[g.dtype], z_q.data_ptr(), fmt, block, z_scales.data_ptr(), act,
+                                  rows, cols, dz.data_ptr(), _ptr(dbias), _ptr(workspace), 0 if workspace is None else
                                   workspace.numel() * workspace.element_size(), _stream(None)))
     return dz, dbias
 
@@ -549,10 +555,10 @@ def hq_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, fmt=E4M3, block=0, q=None
     rows, cols = x.shape
     if weight.dtype not in _DT:
         raise ValueError("weight must be float32, bfloat16 or float16")
-    weight = _like(weight.contiguous(), "weight", (cols,), weight.dtype)
+    weight = _operand(weight, "weight", (cols,), weight.dtype)
     h = x
     if residual is not None:
-        residual = _like(residual.contiguous(), "residual", (rows, cols), x.dtype)
+        residual = _operand(residual, "residual", (rows, cols), x.dtype)
         h = residual_out = _out(residual_out, "residual_out", (rows, cols), x.dtype, x.device)
     elif residual_out is not None:
         raise ValueError("residual_out without a residual: the sum is x itself")
@@ -562,8 +568,9 @@ def hq_rmsnorm_fp8(x, weight, eps=1e-6, residual=None, fmt=E4M3, block=0, q=None
         _like(y_out, "y_out", (rows, cols), x.dtype)
     if rstd_out is not None:
         _like(rstd_out, "rstd_out", (rows,), torch.float32)
-    check(lib.hq_rmsnorm_fp8(_ptr(x), _DT[x.dtype], _ptr(residual), _ptr(weight), _DT[weight.dtype], rows, cols, eps,
-                             fmt, block, _ptr(q), _ptr(scales), _ptr(residual_out), _ptr(y_out), _ptr(rstd_out),
+    check(lib.hq_rmsnorm_fp8(x.data_ptr(), _DT[x.dtype], _ptr(residual), weight.data_ptr(), _DT[weight.dtype], rows,
+                             cols, eps, fmt, block, q.data_ptr(), scales.data_ptr(), _ptr(residual_out), _ptr(y_out),
+                             _ptr(rstd_out),
                              _stream(None)))
     return q, scales, h
 
@@ -586,11 +593,11 @@ def hq_rmsnorm_backward(dy, h, weight, rstd, dres=None, dx=None, dweight=None, n
     rows, cols = dy.shape
     if weight.dtype not in _DT:
         raise ValueError("weight must be float32, bfloat16 or float16")
-    weight = _like(weight.contiguous(), "weight", (cols,), weight.dtype)
-    h = _like(h.contiguous(), "h", (rows, cols), dy.dtype)
-    rstd = _like(rstd.contiguous(), "rstd", (rows,), torch.float32)
+    weight = _operand(weight, "weight", (cols,), weight.dtype)
+    h = _operand(h, "h", (rows, cols), dy.dtype)
+    rstd = _operand(rstd, "rstd", (rows,), torch.float32)
     if dres is not None:
-        dres = _like(dres.contiguous(), "dres", (rows, cols), dy.dtype)
+        dres = _operand(dres, "dres", (rows, cols), dy.dtype)
     dx = _out(dx, "dx", (rows, cols), dy.dtype, dy.device)
     if need_dweight:
         dweight = _out(dweight, "dweight", (cols,), weight.dtype, dy.device)
@@ -599,9 +606,9 @@ def hq_rmsnorm_backward(dy, h, weight, rstd, dres=None, dx=None, dweight=None, n
                                     device=dy.device)
     elif dweight is not None:
         raise ValueError("dweight given with need_dweight=False")
-    check(lib.hq_rmsnorm_backward(_ptr(dy), _ptr(h), _DT[dy.dtype], _ptr(dres), _ptr(weight), _DT[weight.dtype],
-                                  _ptr(rstd), rows, cols, _ptr(dx), _ptr(dweight), _ptr(workspace),
-                                  0 if workspace is None else workspace.numel() * workspace.element_size(),
+    check(lib.hq_rmsnorm_backward(dy.data_ptr(), h.data_ptr(), _DT[dy.dtype], _ptr(dres), weight.data_ptr(),
+                                  _DT[weight.dtype], rstd.data_ptr(), rows, cols, dx.data_ptr(), _ptr(dweight),
+                                  _ptr(workspace), 0 if workspace is None else workspace.numel() * workspace.element_size(),
                                   _stream(None)))
     return dx, dweight
 

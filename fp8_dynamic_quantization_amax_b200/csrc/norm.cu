@@ -229,7 +229,7 @@ __device__ __forceinline__ void ring_init(RingShared& sh, int stages) {
 // in flight into this CTA's shared memory land, or the drain limit passes,
 // before it leaves.  Stages from `stage` on, up to and without next_stage,
 // hold rows not yet waited for; where the two are equal, all of them may.
-// A stage that was never filled in this round has nothing in flight: its
+// A stage that was not filled again has nothing in flight: its
 // wait ends at the limit.
 __device__ __forceinline__ void drain_stages(uint64_t* full, int stages, int stage, uint32_t phase, int next_stage) {
   int dummy = 0;
