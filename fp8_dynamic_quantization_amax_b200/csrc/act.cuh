@@ -11,15 +11,19 @@
 //   gelu'(z) = e Q(a) for z < 0, 1 - e Q(a) for z > 0,
 //              Q(a) ~ P(a) - a / sqrt(2 pi)
 // (Phi(-a) = e erfcx(a / sqrt 2) / 2, and the density is e / sqrt(2 pi)).
-// P and Q are polynomials on [0, 5.6] (Phi(-5.6) = 1.1e-8; a is held there)
-// of degree 11 and 9, fitted by iteratively reweighted least squares in
-// Chebyshev form to the smallest maximum of e |error|: 1.7e-8 and 2.6e-7.
-// The value keeps the higher degree for its small results at negative z
-// (4e-4 of itself at z = -4), the slope is O(1).  A rational form
-// (Abramowitz and Stegun 7.1.26) has fewer terms but a reciprocal more: the
+// P and Q are polynomials on [0, 5.6] (Phi(-5.6) = 1.1e-8; a is held there),
+// fitted by iteratively reweighted least squares in Chebyshev form to the
+// smallest maximum of e |error|; the figures are of the coefficients as they
+// stand, in f32.  P has degree 11 (3.0e-8), for the value's small results at
+// negative z (4e-4 of itself at z = -4).  Q, whose slope is O(1), has two
+// forms.  Gradients in f32 take degree 12 with Q(0) = 1/2 exact (1.1e-8): over
+// z ~ 1.5 N(0, 1) the slope is off by 4.4e-8 of its norm, plain f32 erf and exp
+// by 4.0e-8.  Gradients in bf16 and f16 take degree 9 (2.7e-7; their half steps
+// are 3.9e-3 and 4.9e-4).  At bf16's memory rate the backward kernel has 28
+// cycles per warp-wide element, at f32's 50.  A rational form (Abramowitz and
+// Stegun 7.1.26) has fewer terms but a reciprocal more, and the
 // special-function unit takes 8 cycles of its quarter of an SM for a warp's
-// exp2 or reciprocal, and the backward kernel has 28 cycles per warp-wide
-// element at the memory's rate.
+// exp2 or reciprocal.
 #pragma once
 
 #include "elem.cuh"
@@ -101,22 +105,39 @@ __device__ __forceinline__ float act_clamp(float z, float lim) {
 // |z| = lim every derivative is 0 or 1 to within 1e-7 (1e-26 in the sigmoid
 // forms), so z is held there (NaN passes): e stays finite (lim = 10 gives
 // x = 87 in the tanh form) and no product meets infinity * 0.
-template <int ACT>
+// F32: the result stays in f32 (the erf form's polynomial, above).
+template <int ACT, bool F32>
 __device__ __forceinline__ float2 act_backward(float2 z) {
   if (ACT == kActRelu)
     return make_float2(z.x > 0.0f ? 1.0f : (z.x != z.x ? z.x : 0.0f), z.y > 0.0f ? 1.0f : (z.y != z.y ? z.y : 0.0f));
   if (ACT == kActGelu) {
     float2 e;
     const float2 a = act_gauss(z, e);
-    float2 q = f2_fma(act_both(-8.06304979e-06f), a, act_both(0.000151941553f));
-    q = f2_fma(q, a, act_both(-0.00127115997f));
-    q = f2_fma(q, a, act_both(0.00638279831f));
-    q = f2_fma(q, a, act_both(-0.0222308636f));
-    q = f2_fma(q, a, act_both(0.059496779f));
-    q = f2_fma(q, a, act_both(-0.131772876f));
-    q = f2_fma(q, a, act_both(0.249752298f));
-    q = f2_fma(q, a, act_both(-0.797864914f));
-    q = f2_fma(q, a, act_both(0.499999732f));
+    float2 q;
+    if (F32) {
+      q = f2_fma(act_both(5.99616286e-08f), a, act_both(-1.63705761e-06f));
+      q = f2_fma(q, a, act_both(2.02306855e-05f));
+      q = f2_fma(q, a, act_both(-0.000151731801f));
+      q = f2_fma(q, a, act_both(0.000786682474f));
+      q = f2_fma(q, a, act_both(-0.00307194889f));
+      q = f2_fma(q, a, act_both(0.00968592428f));
+      q = f2_fma(q, a, act_both(-0.0260962807f));
+      q = f2_fma(q, a, act_both(0.0622803979f));
+      q = f2_fma(q, a, act_both(-0.132924139f));
+      q = f2_fma(q, a, act_both(0.249992698f));
+      q = f2_fma(q, a, act_both(-0.797884226f));
+      q = f2_fma(q, a, act_both(0.5f));
+    } else {
+      q = f2_fma(act_both(-8.06304979e-06f), a, act_both(0.000151941553f));
+      q = f2_fma(q, a, act_both(-0.00127115997f));
+      q = f2_fma(q, a, act_both(0.00638279831f));
+      q = f2_fma(q, a, act_both(-0.0222308636f));
+      q = f2_fma(q, a, act_both(0.059496779f));
+      q = f2_fma(q, a, act_both(-0.131772876f));
+      q = f2_fma(q, a, act_both(0.249752298f));
+      q = f2_fma(q, a, act_both(-0.797864914f));
+      q = f2_fma(q, a, act_both(0.499999732f));
+    }
     // 1/2 +- (1/2 - e Q), the sign that of z
     const float2 d = f2_fma(make_float2(-e.x, -e.y), q, act_both(0.5f));
     return f2_add(make_float2(copysignf(d.x, z.x), copysignf(d.y, z.y)), act_both(0.5f));

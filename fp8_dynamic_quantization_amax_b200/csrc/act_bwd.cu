@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(32 * kAbWarps, 4) k_act_bwd(const AbParams p) 
 #pragma unroll
           for (int j = 0; j < kAbVec / 2; ++j) {
             const float2 z = f2_mul(decode2<FMT>((j < 2 ? zc[k].x : zc[k].y) >> (16 * (j & 1))), act_both(sc[k]));
-            d[j] = f2_mul(g[j], act_backward<ACT>(z));
+            d[j] = f2_mul(g[j], act_backward<ACT, GT == 0>(z));
             acc[j] = f2_add(acc[j], d[j]);
           }
           char* dp = static_cast<char*>(p.dz) + (row * p.cols + c0) * elem_bytes<GT>();
