@@ -23,6 +23,7 @@
 #include "hq_internal.cuh"
 #include "launch.cuh"
 #include "ptx.cuh"
+#include "row_grid.cuh"
 
 #include <atomic>
 
@@ -976,7 +977,7 @@ cudaError_t norm_ring(const NormArgs& a, const NormParams& p) {
   if (stages > kRingStages) stages = kRingStages;
   const int64_t most = static_cast<int64_t>(sm_count()) * ctas;
   // a CTA's rows start at one place of a vector: VEC rows apart, or one row
-  const int64_t grid = a.rows <= most ? a.rows : SHIFT ? most / vec_elems<XT>() * vec_elems<XT>() : most;
+  const int64_t grid = row_grid(a.rows, most, SHIFT ? vec_elems<XT>() : 1);
   const int64_t per = (a.rows + grid - 1) / grid;
   if (stages > per) stages = per;
   return launch_pdl(k_rmsnorm_ring<XT, E, RES, SHIFT, false>, dim3(static_cast<unsigned>(grid)), dim3(threads),
@@ -1040,21 +1041,13 @@ int clusters_at_once(K kernel, const ClusterPlan& c, std::atomic<uint64_t>& last
   return fit;
 }
 
-// the clusters to launch: a row each, or as many as run at the same time
-template <int XT, bool SHIFT>
-int64_t cluster_grid(int64_t rows, int64_t most) {
-  constexpr int64_t kVec = vec_elems<XT>();
-  if (rows <= most) return rows;
-  return SHIFT && most >= kVec ? most / kVec * kVec : SHIFT ? kVec : most;
-}
-
 template <int XT, int E, bool RES, bool SHIFT>
 cudaError_t norm_cluster(const NormArgs& a, const NormParams& p, const ClusterPlan& c) {
   static std::atomic<uint64_t> done{0}, last{0};
   const auto kernel = k_rmsnorm_ring<XT, E, RES, SHIFT, true>;
   const cudaError_t e = open_smem(kernel, done);
   if (e != cudaSuccess) return e;
-  const int64_t grid = cluster_grid<XT, SHIFT>(a.rows, clusters_at_once(kernel, c, last));
+  const int64_t grid = row_grid(a.rows, clusters_at_once(kernel, c, last), SHIFT ? vec_elems<XT>() : 1);
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid * c.ctas)), dim3(c.threads), c.smem, a.stream, c.ctas, p,
                             c.stages, device_error_word());
 }
@@ -1102,7 +1095,7 @@ cudaError_t bwd_cluster(const NormBwdArgs& a, const NormBwdParams& p, const Clus
   const auto kernel = k_rmsnorm_bwd_ring<XT, E, DRES, SHIFT, true>;
   const cudaError_t e = open_smem(kernel, done);
   if (e != cudaSuccess) return e;
-  grid = cluster_grid<XT, SHIFT>(a.rows, clusters_at_once(kernel, c, last));  // partial rows too
+  grid = row_grid(a.rows, clusters_at_once(kernel, c, last), SHIFT ? vec_elems<XT>() : 1);  // partial rows too
   return launch_pdl_cluster(kernel, dim3(static_cast<unsigned>(grid * c.ctas)), dim3(c.threads), c.smem, a.stream, c.ctas, p, 1,
                             c.stages, device_error_word());
 }
@@ -1125,9 +1118,8 @@ cudaError_t bwd_ring(const NormBwdArgs& a, const NormBwdParams& p, int64_t& grid
   const int ctas = (T * teams <= half && 2 * teams * stage <= kRingSmem / 2 - kBwdSpare) ? 2 : 1;
   int64_t most = sms * ctas;
   if (most > kBwdParts) most = kBwdParts;
-  grid = (a.rows + teams - 1) / teams;
   // a team's rows start at one place of a vector: VEC rows apart, or one row
-  if (grid > most) grid = SHIFT ? most / vec_elems<XT>() * vec_elems<XT>() : most;
+  grid = row_grid((a.rows + teams - 1) / teams, most, SHIFT ? vec_elems<XT>() : 1);
   const int64_t per = (a.rows + grid * teams - 1) / (grid * teams);
   int64_t stages = (kRingSmem / ctas - kBwdSpare) / (teams * stage);
   if (stages > kRingStages) stages = kRingStages;
