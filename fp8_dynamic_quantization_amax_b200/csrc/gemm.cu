@@ -22,6 +22,7 @@
 // Every wait is bounded: on a stalled barrier the CTA records an error in a
 // device word, drains what it has in flight and exits instead of hanging.
 #include "act.cuh"
+#include "act_tile.cuh"
 #include "fp8_cvt.cuh"
 #include "hq_internal.cuh"
 #include "launch.cuh"
@@ -1504,41 +1505,6 @@ cudaError_t run2(const GemmArgs& a, std::string* msg) {
   if (clusters < 1) clusters = 1;
   return launch_pdl(k_gemm2<KIND, SUBN, NSUB, STAGES, ACT>, dim3(2 * clusters), dim3(gemm_threads<ACT>()), kSmem, a.stream,
                     false, ta, tb, to, p);
-}
-
-// Tile of the activation GEMM for more than 128 rows where the CTA-pair rule
-// below does not hold (ragged N, N < 2048, middling M): the one of the least
-// estimated time,
-//   t_k nkb + (rounds - 1) max(t_k nkb, t_e) + t_e
-// with t_k the time of a 128-byte K block and t_e of a tile's epilogue
-// (silu, bias, residual), us, measured on one round of tiles; the 256 x 512
-// tile has no second accumulator and pays both every round.  All tiles give
-// the same bits.  Against 128 x 128 throughout, us: 692 x 9208 x 28352
-// 244 -> 158 (256 x 512), 1388 x 1880 x 4560 36.9 -> 29.4 and 1460 x 24400 x
-// 1776 118 -> 99 (256 x 256), 133 x 2096 x 1840 12.1 -> 9.5 (128 x 64); the
-// 128 x 128 tile stays ahead at 2047 x 1024 x 4096 (15.1, else 20.4 or more).
-enum ActTile { kT64, kT128, kT256, kPair256, kPair512 };
-ActTile pick_act_tile(int64_t M, int64_t N, int64_t nkb, int64_t sms) {
-  struct Cost {
-    int rows, cols, units;  // units: SMs per tile
-    double k, e;
-  };
-  static constexpr Cost kCosts[] = {{128, 64, 1, 0.27, 2.9},
-                                    {128, 128, 1, 0.385, 4.4},
-                                    {128, 256, 1, 0.44, 8.5},
-                                    {256, 256, 2, 0.42, 8.8},
-                                    {256, 512, 2, 0.75, 18.0}};
-  int best = 0;
-  double least = 0.0;
-  for (int i = 0; i < 5; ++i) {
-    const Cost& c = kCosts[i];
-    const int64_t tiles = ((M + c.rows - 1) / c.rows) * ((N + c.cols - 1) / c.cols);
-    const double rounds = static_cast<double>((tiles + sms / c.units - 1) / (sms / c.units));
-    const double k = c.k * static_cast<double>(nkb);
-    const double t = i == kPair512 ? rounds * (k + c.e) : k + (rounds - 1.0) * (k > c.e ? k : c.e) + c.e;
-    if (i == 0 || t < least) { least = t; best = i; }
-  }
-  return static_cast<ActTile>(best);
 }
 
 // ACT: the kernels with the activation epilogue (dense a8w8; the same tiles).
