@@ -17,8 +17,8 @@
 // stand, in f32.  P has degree 11 (3.0e-8), for the value's small results at
 // negative z (4e-4 of itself at z = -4).  Q, whose slope is O(1), has two
 // forms.  Gradients in f32 take degree 12 with Q(0) = 1/2 exact (1.1e-8): over
-// z ~ 1.5 N(0, 1) the slope is off by 4.4e-8 of its norm, plain f32 erf and exp
-// by 4.0e-8.  Gradients in bf16 and f16 take degree 9 (2.7e-7; their half steps
+// z ~ 1.5 N(0, 1) the slope is off by 4.5e-8 of its norm, plain f32 erf and exp
+// by 4.2e-8.  Gradients in bf16 and f16 take degree 9 (2.7e-7; their half steps
 // are 3.9e-3 and 4.9e-4).  At bf16's memory rate the backward kernel has 28
 // cycles per warp-wide element, at f32's 50.  A rational form (Abramowitz and
 // Stegun 7.1.26) has fewer terms but a reciprocal more, and the

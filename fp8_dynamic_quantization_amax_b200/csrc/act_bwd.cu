@@ -12,8 +12,10 @@
 //
 // Bound: memory, as long as the derivative keeps up (act.cuh says how); four
 // CTAs of 256 threads on an SM hold the loads that this takes.  [16384, 28672]
-// bf16 with dbias, erf GELU: 398-470 us, 6.0-5.1 TB/s (one row in flight and
-// erff: 571 us); [2047, 4096] f16, SiLU: 8.4 us.
+// with dbias, erf GELU: bf16 399 us replayed from a graph, 472 in calls among
+// others at the capped clock, 6.0 and 5.1 TB/s (one row in flight and erff:
+// 571 us); f32 902-918 us, 4.7 TB/s (64 registers spill 52-84 bytes there).
+// [2047, 4096] f16, SiLU: 8.4 us.
 #include "act.cuh"
 #include "elem.cuh"
 #include "hq_internal.cuh"

@@ -13,7 +13,8 @@ namespace hq {
 // with t_k the time of a 128-byte K block and t_e of a tile's epilogue
 // (silu, bias, residual), us, measured on one round of tiles; the 256 x 512
 // tile has no second accumulator and pays both every round.  All tiles give
-// the same bits.  Measured with that epilogue, us, the choice in brackets:
+// the same bits.  Measured with that epilogue and the operands in L2, us, the
+// choice in brackets:
 //                         128x64  128x128  128x256  256x256  256x512
 //    133 x  2096 x  1840   [9.3]     11.9     17.2     16.4     25.6
 //   2047 x  1024 x  4096    20.3   [14.8]     19.8     21.3     34.1

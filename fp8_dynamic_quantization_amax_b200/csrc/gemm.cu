@@ -1515,10 +1515,12 @@ cudaError_t dispatch_gemm(const GemmArgs& a, std::string* msg) {
   // tile once N is large enough
   const bool wide = ((a.N % 256 == 0) && a.N >= 2048 && a.M >= 256) || (a.offsets != nullptr && a.N >= 1024);
   // Large dense GEMMs run on CTA pairs (256 x 256 tiles).  Below M = 4096
-  // only with much work: for M of 1024 to some 3000 at K = 1024 .. 4096 the 1-CTA
-  // 128 x 256 tiles measured 2-7 % faster (the pair's set-up and coarser
-  // last round weigh more in a 15-40 us GEMM); at M = 2048, N = 28672,
-  // K = 8192 the pair was 3 % faster.
+  // only with much work: the pair's set-up and coarser last round weigh more
+  // in a short GEMM.  1-CTA 128 x 256 tiles and the pair, us: 2048 x 4096 x
+  // 1024 11.7 and 12.5, 2816 x 4096 x 1024 15.7 and 15.9, 1024 x 8192 x 1024
+  // 11.8 and 12.5; even at K = 4096 (2048 x 4096 28.3 and 28.1, 2816 x 4096
+  // 42.2 and 41.4); 1024 x 8192 x 8192, below the threshold, 63.4 and 60.1;
+  // 512 x 28672 x 8192 138 and 122, 2048 x 28672 x 8192 387 and 362.
   const bool pair = a.offsets == nullptr && a.kind == 0 && (a.N % 256 == 0) && a.N >= 2048 &&
                     (a.M >= 4096 || (a.M >= 512 && static_cast<double>(a.M) * a.N * a.K >= 137438953472.0));  // 2^37
   // 256 x 512 pair tiles read a quarter fewer operand bytes per flop; with

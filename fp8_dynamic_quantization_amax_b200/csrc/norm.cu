@@ -14,10 +14,11 @@
 // of f32 sums; a second launch adds the CTAs' partials in CTA order, so the
 // sum has a fixed order and the workspace needs no initial state.
 //
-// Bound: memory where a row brings two tensors or more ([16384, 8192] bf16:
-// 145-159 us with a residual, 6.5-5.9 TB/s; backward 153-163 us, 7.0-6.6
-// TB/s, part of it from L2), instruction issue and the row's serial steps
-// (sum, maximum, divisions) for one tensor a row (97 us, 4.1 TB/s).
+// Bound: memory where a row brings two tensors or more ([16384, 8192] bf16
+// with a residual: 144 us replayed from a graph, 161 in calls among others, 6.5
+// and 5.8 TB/s; backward 156 and 165 us, 6.9 and 6.5 TB/s, part of it from
+// L2), the latency of the row's serial steps (sum, maximum, divisions) with
+// few rows in flight for one tensor a row (93 us, 4.3 TB/s).
 #include "elem.cuh"
 #include "fp8_cvt.cuh"
 #include "hq_internal.cuh"

@@ -571,8 +571,12 @@ hq_status hq_act_backward_fp8(const void* g, hq_dtype gt, const uint8_t* z_q, hq
  *                 be x or residual itself
  *   y_out         device [rows, cols] of xt or NULL: y rounded to x's dtype
  *   rstd_out      device f32 [rows] or NULL (the backward pass reads it)
- *   Every buffer is aligned to its element size; where all rows also start
- *   on 16-byte boundaries (weight and q likewise) the vector path runs.
+ *   Every buffer is aligned to its element size.  The vector path runs where x,
+ *   residual, residual_out and y_out start on 16-byte boundaries and q on one
+ *   of a vector's elements (4 for f32, 8 otherwise): with block == 0 at any
+ *   width of at least three vectors, with blocks where the weight starts on
+ *   a 16-byte boundary and a block is 2, 4, 8, 16 or 32 vectors.  Most other
+ *   calls take one element at a time.
  * rows == 0 or cols == 0 returns HQ_OK with no launch.
  * Errors: HQ_ERR_INVALID_ARG, HQ_ERR_MISALIGNED, HQ_ERR_OVERLAP
  *   (residual_out equal to x or residual excepted), HQ_ERR_WRONG_DEVICE,
